@@ -431,6 +431,124 @@ int w4a8_fused_moe_prepacked_noalloc(const void* hidden_bf16, int64_t T, int64_t
                                      void* out_bf16, hipStream_t stream);
 
 /*
+ * Element types of the operands below that come in more than one type.
+ */
+#define W4A8_TYPE_FP32 0
+#define W4A8_TYPE_BF16 1
+#define W4A8_TYPE_FP16 2
+
+/*
+ * w4a8_moe_route -- router scores to the topk_ids / topk_weights the fused
+ * forward reads.  For token t and expert e, x = logits[t, e]:
+ *   score     sigmoid(x), or softmax over the row's experts
+ *   choice    score + bias[e]   (the balance bias chooses, it does not weigh)
+ *   experts   an expert can be chosen unless its logit or its choice is NaN
+ *             or -inf (a masked or offline expert; such a logit counts as 0 in
+ *             the softmax; +inf logits share the softmax equally)
+ *   groups    the experts are num_groups runs of E/num_groups; a group counts
+ *             by the sum of its best group_top choices (1 or 2; of those that
+ *             can be chosen), and only the topk_groups best groups stay
+ *   topk_ids  the topk largest choices left, in descending order
+ *   weights   scale * score, divided by the sum of the chosen scores if
+ *             renormalize (all 0 if that sum is 0)
+ * Ties, of groups and of experts, go to the lower index.  Choices are compared
+ * by their values to 64 bits (without a bias, and without sums of two, by the
+ * logits themselves, which order the scores exactly); weights are rounded once
+ * to fp32.  Where fewer than topk experts can be chosen, the slots left over
+ * hold id -1 and weight 0, which the fused forward skips.
+ *   logits       [T, E] of logits_type (any of the three), row stride
+ *                ld_logits >= E elements
+ *   bias         [E] fp32, or NULL
+ *   score        W4A8_SCORE_SIGMOID or W4A8_SCORE_SOFTMAX
+ *   num_tokens   device int32, or NULL for T: rows from *num_tokens on (the
+ *                padding of a batch of fixed size, e.g. in a captured graph)
+ *                get id -1 and weight 0 and their logits are not read
+ *   topk_ids     [T, topk] int32;  topk_weights [T, topk] fp32
+ * T >= 0 (T == 0 launches nothing), 1 <= topk <= 32, topk <= topk_groups *
+ * E/num_groups, 1 <= topk_groups <= num_groups, num_groups divides E
+ * (INVALID_ARG otherwise); E <= 1024, T < 2^31, num_groups <= 64, num_tokens
+ * 4-byte aligned, pointers 16-byte aligned (UNSUPPORTED otherwise).  Any row
+ * stride; rows of 16-byte aligned start and length are read with wide loads.
+ */
+#define W4A8_SCORE_SIGMOID 0
+#define W4A8_SCORE_SOFTMAX 1
+int w4a8_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ld_logits,
+                   const float* bias, int score, int64_t num_groups, int64_t topk_groups,
+                   int group_top, int64_t topk, int renormalize, float scale,
+                   const int32_t* num_tokens, int32_t* topk_ids, float* topk_weights,
+                   hipStream_t stream);
+
+/*
+ * w4a8_norm_residual -- what stands between two blocks, in one pass: the norm
+ * after a block, its gate and the residual sum, then the norm before the next
+ * block with its fp8 quantisation.  Per row of H elements, in fp32:
+ *   u    = x * rsqrt(mean(x^2) + eps) * (post_weight + weight_offset)
+ *          (post_weight NULL: u = x)
+ *   r'   = residual_scale * residual + gate * u
+ *          (gate NULL: 1; residual NULL: r' = gate * u; x NULL: r' =
+ *          residual_scale * residual)
+ *   y    = r' * rsqrt(mean(r'^2) + eps) * (pre_weight + weight_offset)
+ * with y taken from r' before it is rounded; every output is rounded once.
+ *   x            [T, H] fp32 or bf16 (x_type), row stride ldx, or NULL
+ *   residual     [T, H] fp32 or bf16 (residual_type), row stride ldr, or NULL
+ *   post_weight, pre_weight  [H], gate: fp32 or bf16, all of param_type; each
+ *                may be NULL
+ *   gate         element (t, h) at gate[t * gate_row_stride + h *
+ *                gate_col_stride]: row stride 0 for one gate for all tokens,
+ *                column stride 1, or 0 for one value per token
+ *   residual_out [T, H] of residual_type, row stride ldr_out, or NULL: r'.
+ *                It may be `residual` itself (same stride)
+ *   y_bf16       [T, H] bf16, row stride ldy, or NULL
+ *   q_e4m3       [T, H] e4m3 codes of y, row stride H, with
+ *   q_scales     [T, H/128] fp32, by the rule of w4a8_quantize_act on the
+ *                unrounded y; both or neither
+ * T >= 0 (T == 0 launches nothing), H > 0, eps > 0; pre_weight and an output
+ * of y go together, and so do a missing pre_weight and none; x or residual
+ * must be given, and some output; post_weight and gate need x (INVALID_ARG
+ * otherwise).  H <= 32768, T < 2^31, H % 128 == 0 with codes, pointers
+ * 16-byte aligned (UNSUPPORTED otherwise).  Any row strides >= H; rows whose
+ * start is 16-byte aligned are read and written with wide accesses.  Squares
+ * are summed in fp32: |values| stay below 2^56.
+ */
+int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* residual,
+                       int residual_type, int64_t ldr, int64_t T, int64_t H, int param_type,
+                       const void* post_weight, const void* gate, int64_t gate_row_stride,
+                       int64_t gate_col_stride, float residual_scale, const void* pre_weight,
+                       float weight_offset, float eps, void* residual_out, int64_t ldr_out,
+                       void* y_bf16, int64_t ldy, uint8_t* q_e4m3, float* q_scales,
+                       hipStream_t stream);
+
+/*
+ * w4a8_gemm_epilogue -- the dense W4AFP8 linear of w4a8_gemm with its
+ * epilogue: out = bf16(act(A * W^T + bias) + residual), rounded once.
+ *   a_e4m3, a_scales, b_int4, b_scales  as in w4a8_gemm; b has R rows, R = N,
+ *                or R = 2N with W4A8_ACT_SWIGLU: gate rows [0, N), up rows
+ *                [N, 2N), act = silu(gate) * up
+ *   bias         [R] fp32 or bf16 (bias_type), or NULL; added before act
+ *   activation   W4A8_ACT_*: none, max(y, 0), y * sigmoid(y), y * Phi(y)
+ *                (exact and tanh form), and SwiGLU
+ *   residual     [M, N] bf16, row stride ld_residual >= N, or NULL; it may be
+ *                out itself (same stride)
+ *   out_bf16     [M, N], row stride ld_out >= N
+ *   workspace    device scratch of *workspace_bytes bytes (query with NULL; it
+ *                depends on M, K, N and activation alone, and may be 0)
+ * M >= 0 (M == 0 launches nothing), N > 0, K > 0 (INVALID_ARG otherwise), K %
+ * 128 == 0, K <= 2^22, M, R < 2^31, pointers 16-byte aligned (UNSUPPORTED
+ * otherwise).  Operands may exceed 2^32 bytes.
+ */
+#define W4A8_ACT_NONE 0
+#define W4A8_ACT_RELU 1
+#define W4A8_ACT_SILU 2
+#define W4A8_ACT_GELU 3
+#define W4A8_ACT_GELU_TANH 4
+#define W4A8_ACT_SWIGLU 5
+int w4a8_gemm_epilogue(const uint8_t* a_e4m3, const float* a_scales, int64_t M, int64_t K,
+                       const uint8_t* b_int4, const float* b_scales, int64_t N, const void* bias,
+                       int bias_type, int activation, const void* residual_bf16,
+                       int64_t ld_residual, void* out_bf16, int64_t ld_out, void* workspace,
+                       size_t* workspace_bytes, hipStream_t stream);
+
+/*
  * w4a8_fused_moe_workspace_layout -- where w4a8_fused_moe keeps its
  * intermediates inside the workspace (host-only query, no HIP call), so that
  * tests and tools can read them after a call:

@@ -5,6 +5,7 @@
 // synchronisation, no state between calls.
 #include "w4a8.h"
 
+#include "api_util.hpp"
 #include "internal.hpp"
 
 #include <algorithm>
@@ -14,31 +15,9 @@
 
 namespace {
 
+using namespace w4a8::api;
+
 constexpr int64_t kMaxLocalExperts = 1024;
-constexpr size_t kAlign = 256;
-
-inline size_t round_up(size_t x)
-{
-    return (x + kAlign - 1) / kAlign * kAlign;
-}
-inline bool aligned16(const void* p)
-{
-    return ((uintptr_t)p & 15u) == 0;
-}
-
-// A bump allocator over the caller's workspace (or over nothing, to size it).
-struct Carve {
-    char* base;
-    size_t used = 0;
-    explicit Carve(void* b) : base((char*)b) {}
-    template <typename T>
-    T* take(size_t count)
-    {
-        T* p = base ? (T*)(base + used) : nullptr;
-        used += round_up(count * sizeof(T));
-        return p;
-    }
-};
 
 // rows per m-block for the skinny grouped GEMM: from the pairs each local
 // expert would get if every pair were local (the host does not see the routing)
@@ -50,11 +29,6 @@ int pick_block_m(int64_t pairs, int64_t experts)
     if (per <= 32)
         return 32;
     return 64;
-}
-
-int64_t ceil_div(int64_t a, int64_t b)
-{
-    return (a + b - 1) / b;
 }
 
 // Between the decode regime (at most 16 pairs per expert: 16-row blocks) and
@@ -256,35 +230,6 @@ inline bool below_u32(int64_t bytes)
 {
     return bytes >= 0 && bytes < kRangeLimit;
 }
-// products of non-negative sizes without int64 overflow (limit 2^62)
-inline int64_t mul_sat(int64_t a, int64_t b)
-{
-    const int64_t cap = (int64_t)1 << 62;
-    if (a <= 0 || b <= 0)
-        return 0;
-    return a > cap / b ? cap : a * b;
-}
-
-int check_workspace(void* ws, size_t* bytes, size_t need)
-{
-    if (bytes == nullptr)
-        return W4A8_ERR_INVALID_ARG;
-    if (ws == nullptr) {
-        *bytes = need;
-        return W4A8_OK;
-    }
-    if (*bytes < need)
-        return W4A8_ERR_WORKSPACE;
-    if (!aligned16(ws))
-        return W4A8_ERR_UNSUPPORTED;
-    return -1;  // proceed
-}
-
-inline int hip_status(hipError_t e)
-{
-    return e == hipSuccess ? W4A8_OK : W4A8_ERR_HIP;
-}
-
 // events armed by w4a8_fused_moe_stage_events for the next call on this
 // thread (the handles are copied, the caller's array may go away)
 thread_local void* t_stage_events[6] = {nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};

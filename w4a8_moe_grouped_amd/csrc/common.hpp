@@ -227,6 +227,14 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f)
     return (uint16_t)(u >> 16);
 }
 
+// two fp32 -> packed bf16 (a in the low half), round to nearest even, NaN kept
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float a, float b)
+{
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), b2));
+}
+
 // butterfly reductions over aligned lane groups of width W (power of two <= 64)
 template <int W>
 __device__ __forceinline__ float group_max(float v)

@@ -201,4 +201,64 @@ hipError_t launch_fused_tail(const GemmArgs& gu, const GemmArgs& dn, const TailA
 hipError_t launch_combine(const float* y2, const int32_t* src2dst, const float* topk_w,
                           int64_t T, int64_t topk, int64_t H, uint16_t* out, hipStream_t s);
 
+// ---- router (route.hip) ----
+struct RouteArgs {
+    const void* logits;
+    int type;  // W4A8_TYPE_*
+    int64_t T, ld;
+    int32_t E;
+    const float* bias;  // [E] or null
+    int softmax;        // score: softmax, else sigmoid
+    int32_t groups, kept, group_top;
+    int32_t topk;
+    int renorm;
+    float scale;
+    const int32_t* num_tokens;  // device, or null
+    int32_t* ids;               // [T, topk]
+    float* weights;             // [T, topk]
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+
+// ---- norms around a block (norm.hip) ----
+struct NormArgs {
+    const void* x;         // [T, H] or null
+    const void* residual;  // [T, H] or null
+    int x_type, r_type, p_type;
+    int64_t ldx, ldr, ldr_out, ldy;
+    int64_t T;
+    int32_t H;
+    const void* post_w;  // [H] or null
+    const void* gate;    // null, or element (t, h) at t * gate_rs + h * gate_cs
+    int64_t gate_rs, gate_cs;
+    float r_scale;
+    const void* pre_w;  // [H], or null: no y
+    float w_offset, eps;
+    void* r_out;      // of r_type, or null
+    uint16_t* y;      // bf16 or null
+    uint8_t* q;       // e4m3 codes [T, H] with q_scales [T, H/128], or null
+    float* q_scales;
+    int aligned;  // every row starts at a multiple of 16 bytes
+};
+constexpr int64_t kNormMaxH = 32768;
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+
+// ---- dense linear with an epilogue (dense_epilogue.hip) ----
+struct DenseArgs {
+    const uint8_t* a;  // [M, K] e4m3 codes
+    const float* sa;   // [M, K/128]
+    const uint8_t* w;  // [R, K/2] int4; R = N, or 2N with SwiGLU (gate rows, then up rows)
+    const float* sw;   // [R, K/128]
+    int64_t M, K, N;
+    const void* bias;  // [R] or null
+    int bias_bf16;
+    int act;  // W4A8_ACT_*
+    const uint16_t* residual;  // bf16 or null
+    int64_t ldr;
+    uint16_t* out;
+    int64_t ldo;
+    int vec4;  // four columns of a row are 8-byte aligned in out and residual, N % 4 == 0
+};
+size_t dense_epilogue_workspace(int64_t M, int64_t K, int64_t N, int act);
+hipError_t launch_dense_epilogue(const DenseArgs& a, void* ws, hipStream_t s);
+
 } // namespace w4a8

@@ -8,6 +8,7 @@ exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -25,7 +26,7 @@ EXPORTS = ("w4a8_version", "w4a8_status_string", "w4a8_quantize_act", "w4a8_gemm
            "w4a8_fused_moe_prepacked", "w4a8_prepack_weights_fp4", "w4a8_fused_moe_fp4_prepacked",
            "w4a8_prepack_weights_bf16_scales", "w4a8_fused_moe_prepacked_static",
            "w4a8_fused_moe_recipe", "w4a8_fused_moe_prepacked_noalloc", "w4a8_fused_moe_bounded",
-           "w4a8_fused_moe_persistent")
+           "w4a8_fused_moe_persistent", "w4a8_moe_route", "w4a8_norm_residual", "w4a8_gemm_epilogue")
 
 _lock = threading.Lock()
 _lib = None
@@ -92,6 +93,16 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                                       ctypes.POINTER(ctypes.c_int64)]
         L.w4a8_fused_moe_stage_events.restype = ctypes.c_int
         L.w4a8_fused_moe_stage_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int]
+        ci, f32 = ctypes.c_int, ctypes.c_float
+        L.w4a8_moe_route.restype = ci
+        L.w4a8_moe_route.argtypes = [vp, ci, i64, i64, i64, vp, ci, i64, i64, ci, i64, ci, f32, vp, vp,
+                                     vp, vp]
+        L.w4a8_norm_residual.restype = ci
+        L.w4a8_norm_residual.argtypes = [vp, ci, i64, vp, ci, i64, i64, i64, ci, vp, vp, i64, i64, f32,
+                                         vp, f32, f32, vp, i64, vp, i64, vp, vp, vp]
+        L.w4a8_gemm_epilogue.restype = ci
+        L.w4a8_gemm_epilogue.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, ci, ci, vp, i64, vp, i64,
+                                         vp, sz, vp]
         if path is None:
             _lib = L
         return L
@@ -444,6 +455,230 @@ def moe_align(topk_ids: torch.Tensor, expert_begin: int, num_local_experts: int,
                                  _ptr(o["num_blocks"]), _ptr(ws), ctypes.byref(n), _stream(dev)),
            "w4a8_moe_align")
     return o
+
+
+# ---- the operators around the expert forward -----------------------------------------
+
+TYPE_FP32, TYPE_BF16, TYPE_FP16 = 0, 1, 2
+_TYPES = {torch.float32: TYPE_FP32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16}
+SCORES = {"sigmoid": 0, "softmax": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
+
+
+def _type(t: torch.Tensor, *allowed) -> int:
+    if t.dtype not in allowed:
+        raise W4A8Error("unsupported tensor type %s" % t.dtype)
+    return _TYPES[t.dtype]
+
+
+def _rows(t: torch.Tensor, shape, what: str) -> int:
+    """Row stride of a 2-D tensor of that shape with unit column stride."""
+    if t.shape != shape or (t.stride(1) != 1 and shape[1] > 1):
+        raise W4A8Error("%s must be %s with unit column stride" % (what, tuple(shape)))
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(t: Optional[torch.Tensor], n: int, what: str):
+    if t is not None and (t.shape != (n,) or not t.is_contiguous()):
+        raise W4A8Error("%s must be a contiguous [%d] tensor" % (what, n))
+
+
+def _addr(t: Optional[torch.Tensor], device: torch.device):
+    if t is None:
+        return None
+    if t.device != device:
+        raise W4A8Error("all tensors must be on one GPU")
+    return t.data_ptr()
+
+
+def _launch(device: torch.device, name: str, *args):
+    """One call on the current stream of `device`, with that device current."""
+    fn = getattr(load(), name)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+
+
+def moe_route(logits: torch.Tensor, topk: int, score: str = "sigmoid", bias: Optional[torch.Tensor] = None,
+              num_groups: int = 1, topk_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+              scale: float = 1.0, num_tokens: Optional[torch.Tensor] = None,
+              topk_ids: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None):
+    """w4a8_moe_route: router logits [T, E] (fp32, bf16 or fp16) -> (topk_ids
+    int32 [T, topk], topk_weights fp32 [T, topk]) as the fused forward reads
+    them.  bias: fp32 [E], added to the scores that choose; num_tokens: a
+    one-element int32 device tensor, rows from it on get id -1 and weight 0."""
+    _need_cuda(logits)
+    if logits.dim() != 2 or score not in SCORES:
+        raise W4A8Error("logits must be [T, E] and score one of %s" % (tuple(SCORES),))
+    T, E = logits.shape
+    dev = logits.device
+    ld = _rows(logits, (T, E), "logits")
+    kind = _type(logits, torch.float32, torch.bfloat16, torch.float16)
+    if bias is not None:
+        _vector(bias, E, "bias")
+        _type(bias, torch.float32)
+    if num_tokens is not None and (num_tokens.numel() != 1 or num_tokens.dtype != torch.int32):
+        raise W4A8Error("num_tokens must be one int32")
+    if topk_ids is None:
+        topk_ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    elif topk_ids.shape != (T, topk) or topk_ids.dtype != torch.int32 or not topk_ids.is_contiguous():
+        raise W4A8Error("topk_ids must be a contiguous int32 [T, topk] tensor")
+    if topk_weights is None:
+        topk_weights = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    elif topk_weights.shape != (T, topk) or topk_weights.dtype != torch.float32 or \
+            not topk_weights.is_contiguous():
+        raise W4A8Error("topk_weights must be a contiguous fp32 [T, topk] tensor")
+    _launch(dev, "w4a8_moe_route", logits.data_ptr(), kind, T, E, ld, _addr(bias, dev), SCORES[score],
+            num_groups, topk_groups, group_top, topk, 1 if renormalize else 0, scale,
+            _addr(num_tokens, dev), _addr(topk_ids, dev), _addr(topk_weights, dev))
+    return topk_ids, topk_weights
+
+
+def norm_residual(x: Optional[torch.Tensor], residual: Optional[torch.Tensor],
+                  post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  residual_scale: float = 1.0, pre_weight: Optional[torch.Tensor] = None,
+                  weight_offset: float = 0.0, eps: float = 1e-6, quantize: bool = False,
+                  keep_residual: bool = True, residual_out: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, out_scales: Optional[torch.Tensor] = None):
+    """w4a8_norm_residual: r' = residual_scale * residual + gate * norm(x) and
+    y = norm(r'), in one pass.  x and residual: [T, H] fp32 or bf16, either may
+    be None; post_weight, pre_weight [H] and gate ([H], [T, 1] or [T, H]): fp32
+    or bf16, of one type.  Returns (r' of residual's type (x's without one) or
+    None, y or None, scales or None): y is bf16 [T, H], or with quantize uint8
+    e4m3 codes with their fp32 [T, H/128] scales, as quantize_act makes them;
+    None without pre_weight.  keep_residual=False: r' is not written.
+    residual_out, out and out_scales may be given; residual_out may be
+    residual itself."""
+    lead = x if x is not None else residual
+    if lead is None:
+        raise W4A8Error("x or residual must be given")
+    _need_cuda(lead)
+    if lead.dim() != 2:
+        raise W4A8Error("x and residual must be [T, H]")
+    T, H = shape = lead.shape
+    dev = lead.device
+    rows = (torch.float32, torch.bfloat16)
+    ldx = ldr = H
+    x_type = r_type = TYPE_BF16
+    if x is not None:
+        ldx, x_type = _rows(x, shape, "x"), _type(x, *rows)
+    r_like = lead if residual is None else residual
+    r_type = _type(r_like, *rows)
+    if residual is not None:
+        ldr = _rows(residual, shape, "residual")
+    params = [p for p in (post_weight, pre_weight, gate) if p is not None]
+    p_type = _type(params[0], *rows) if params else TYPE_FP32
+    if any(p.dtype != params[0].dtype for p in params):
+        raise W4A8Error("post_weight, pre_weight and gate must be of one type")
+    _vector(post_weight, H, "post_weight")
+    _vector(pre_weight, H, "pre_weight")
+    gate_rs = gate_cs = 0
+    if gate is not None:
+        if gate.shape == (H,) and gate.is_contiguous():
+            gate_cs = 1
+        elif gate.shape == (T, H):
+            gate_rs, gate_cs = _rows(gate, shape, "gate"), 1
+        elif gate.shape == (T, 1):
+            gate_rs = gate.stride(0) if T > 1 else 1
+        else:
+            raise W4A8Error("gate must be a contiguous [H], or [T, H] or [T, 1]")
+    if residual_out is None:
+        if keep_residual:
+            residual_out = torch.empty(shape, dtype=r_like.dtype, device=dev)
+    elif residual_out.dtype != r_like.dtype or not keep_residual:
+        raise W4A8Error("residual_out must have the residual's type")
+    ldr_out = H if residual_out is None else _rows(residual_out, shape, "residual_out")
+    ldy, y_ptr, q_ptr = H, None, None
+    if pre_weight is None:
+        if quantize or out is not None or out_scales is not None:
+            raise W4A8Error("an output y needs pre_weight")
+    elif quantize:
+        if H % GROUP != 0:
+            raise W4A8Error("quantize needs H %% %d == 0" % GROUP)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.uint8, device=dev)
+        if out_scales is None:
+            out_scales = torch.empty((T, H // GROUP), dtype=torch.float32, device=dev)
+        if out.shape != shape or out.dtype != torch.uint8 or not out.is_contiguous() or \
+                out_scales.shape != (T, H // GROUP) or out_scales.dtype != torch.float32 or \
+                not out_scales.is_contiguous():
+            raise W4A8Error("out must be uint8 [T, H] and out_scales fp32 [T, H/128], contiguous")
+        q_ptr = _addr(out, dev)
+    else:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        _type(out, torch.bfloat16)
+        if out_scales is not None:
+            raise W4A8Error("out_scales needs quantize")
+        ldy, y_ptr = _rows(out, shape, "out"), _addr(out, dev)
+    _launch(dev, "w4a8_norm_residual", _addr(x, dev), x_type, ldx, _addr(residual, dev), r_type, ldr, T, H,
+            p_type, _addr(post_weight, dev), _addr(gate, dev), gate_rs, gate_cs, residual_scale,
+            _addr(pre_weight, dev), weight_offset, eps, _addr(residual_out, dev), ldr_out, y_ptr, ldy,
+            q_ptr, _addr(out_scales, dev))
+    return residual_out, out, out_scales
+
+
+@functools.lru_cache(maxsize=1024)
+def gemm_epilogue_workspace_bytes(M: int, K: int, N: int, activation: str = "none") -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().w4a8_gemm_epilogue(None, None, M, K, None, None, N, None, 0, ACTIVATIONS[activation], None,
+                                     N, None, N, None, ctypes.byref(n), None), "w4a8_gemm_epilogue(query)")
+    return n.value
+
+
+def gemm_epilogue(a_q: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                  bias: Optional[torch.Tensor] = None, activation: str = "none",
+                  residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None):
+    """w4a8_gemm_epilogue: bf16 [M, N] = act(A * W^T + bias) + residual.  a_q,
+    a_scales, w, w_scales as for gemm; with activation "swiglu" w has 2N rows
+    (gate rows, then up rows).  bias: fp32 or bf16, one value per weight row;
+    residual: bf16 [M, N], may be out itself."""
+    _need_cuda(a_q)
+    if activation not in ACTIVATIONS:
+        raise W4A8Error("activation must be one of %s" % (tuple(ACTIVATIONS),))
+    if a_q.dim() != 2 or w.dim() != 2:
+        raise W4A8Error("a_q must be [M, K] and w [rows, K/2]")
+    M, K = a_q.shape
+    R = w.shape[0]
+    N = R // 2 if activation == "swiglu" else R
+    dev = a_q.device
+    if w.shape[1] * 2 != K or a_scales.shape != (M, K // GROUP) or w_scales.shape != (R, K // GROUP) or \
+            (activation == "swiglu" and R % 2 != 0):
+        raise W4A8Error("bad operand shapes")
+    if a_q.dtype != torch.uint8 or w.dtype != torch.uint8 or a_scales.dtype != torch.float32 or \
+            w_scales.dtype != torch.float32:
+        raise W4A8Error("codes and weights must be uint8, their scales fp32")
+    if not (a_q.is_contiguous() and a_scales.is_contiguous() and w.is_contiguous() and w_scales.is_contiguous()):
+        raise W4A8Error("operands must be contiguous")
+    bias_type = TYPE_FP32
+    if bias is not None:
+        _vector(bias, R, "bias")
+        bias_type = _type(bias, torch.float32, torch.bfloat16)
+    ldr = N
+    if residual is not None:
+        _type(residual, torch.bfloat16)
+        ldr = _rows(residual, (M, N), "residual")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _type(out, torch.bfloat16)
+    ldo = _rows(out, (M, N), "out")
+    if workspace is None:
+        need = gemm_epilogue_workspace_bytes(M, K, N, activation)
+        # a call that needs none still names a buffer (NULL asks for the size)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else out
+        n = ctypes.c_size_t(need)
+    else:
+        n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    if M == 0:
+        return out
+    _launch(dev, "w4a8_gemm_epilogue", a_q.data_ptr(), _addr(a_scales, dev), M, K, _addr(w, dev),
+            _addr(w_scales, dev), N, _addr(bias, dev), bias_type, ACTIVATIONS[activation],
+            _addr(residual, dev), ldr, _addr(out, dev), ldo, _addr(workspace, dev), ctypes.byref(n))
+    return out
 
 
 STAGES = ("align", "quant", "gate_up", "down", "combine")
