@@ -210,6 +210,7 @@ struct RouteArgs {
     const float* bias;  // [E] or null
     int softmax;        // score: softmax, else sigmoid
     int32_t groups, kept, group_top;
+    int wide;           // set by the launcher: rows allow wide loads
     int32_t topk;
     int renorm;
     float scale;
