@@ -101,6 +101,26 @@ def test_route_masked_and_special_values(dev, score, groups, kept):
     for b in (None, bias, special):
         for top in (1, 2):
             check_route(x, k, score=score, bias=b, num_groups=groups, topk_groups=kept, group_top=top)
+            check_route(x, k, score=score, bias=b, num_groups=groups, topk_groups=kept, group_top=top,
+                        renormalize=False)
+            check_route(x.to(FP16), 12, score=score, bias=b, num_groups=groups, topk_groups=kept, group_top=top)
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("E, groups, kept", [(256, 8, 4), (256, 16, 5), (256, 2, 1), (192, 6, 2), (64, 8, 3), (128, 4, 2),
+                                             (100, 1, 1), (250, 1, 1)])
+def test_route_near_ties(dev, dtype, E, groups, kept):
+    """Logits a few steps of their type apart, and sums of choices whose parts
+    cancel: the order is that of 64 bits."""
+    g = gen(dev, E + groups)
+    step = torch.finfo(dtype).eps
+    x = (1 + step * torch.randint(0, 9, (60, E), generator=g, device=dev)).to(dtype)
+    x[30:] *= -1
+    wide = 1000 * torch.randint(-1, 2, (E,), generator=g, device=dev).float()
+    for score in ("sigmoid", "softmax"):
+        for bias in (None, torch.zeros(E, device=dev), wide, 1e-7 * torch.randn(E, generator=g, device=dev)):
+            for top in (1, 2):
+                check_route(x, 8, score=score, bias=bias, num_groups=groups, topk_groups=kept, group_top=top)
 
 
 def test_route_orders_scores_that_32_bits_round_alike(dev):

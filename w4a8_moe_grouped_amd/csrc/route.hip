@@ -29,24 +29,32 @@ namespace {
 constexpr int kRWaves = 4;  // tokens per workgroup
 constexpr double kNone = -__builtin_inf();
 
+// A constant in scalar registers: a 64-bit fma takes one such operand, where a
+// literal would first be moved into a pair of vector registers.
+__device__ __forceinline__ double in_sgprs(double c)
+{
+    asm("" : "+s"(c));
+    return c;
+}
+
 // exp to 64 bits for z in [-800, 709]: 2^n * e^r, |r| <= ln(2)/2, by the
 // Taylor sum to r^13/13! (the rest is below 4e-18)
 __device__ __forceinline__ double exp64(double z)
 {
-    const double n = __builtin_rint(z * 1.4426950408889634);
-    double r = fma(n, -0x1.62e42fefa0000p-1, z);  // ln 2 to 38 bits, exact times n
-    r = fma(n, -0x1.cf79abc9e3b3ap-40, r);           // the rest of it
-    double p = 1.0 / 6227020800.0;
-    p = fma(p, r, 1.0 / 479001600.0);
-    p = fma(p, r, 1.0 / 39916800.0);
-    p = fma(p, r, 1.0 / 3628800.0);
-    p = fma(p, r, 1.0 / 362880.0);
-    p = fma(p, r, 1.0 / 40320.0);
-    p = fma(p, r, 1.0 / 5040.0);
-    p = fma(p, r, 1.0 / 720.0);
-    p = fma(p, r, 1.0 / 120.0);
-    p = fma(p, r, 1.0 / 24.0);
-    p = fma(p, r, 1.0 / 6.0);
+    const double n = __builtin_rint(z * in_sgprs(1.4426950408889634));
+    double r = fma(n, in_sgprs(-0x1.62e42fefa0000p-1), z);  // ln 2 to 38 bits, exact times n
+    r = fma(n, in_sgprs(-0x1.cf79abc9e3b3ap-40), r);        // the rest of it
+    double p = in_sgprs(1.0 / 6227020800.0);
+    p = fma(p, r, in_sgprs(1.0 / 479001600.0));
+    p = fma(p, r, in_sgprs(1.0 / 39916800.0));
+    p = fma(p, r, in_sgprs(1.0 / 3628800.0));
+    p = fma(p, r, in_sgprs(1.0 / 362880.0));
+    p = fma(p, r, in_sgprs(1.0 / 40320.0));
+    p = fma(p, r, in_sgprs(1.0 / 5040.0));
+    p = fma(p, r, in_sgprs(1.0 / 720.0));
+    p = fma(p, r, in_sgprs(1.0 / 120.0));
+    p = fma(p, r, in_sgprs(1.0 / 24.0));
+    p = fma(p, r, in_sgprs(1.0 / 6.0));
     p = fma(p, r, 0.5);
     p = fma(p, r, 1.0);
     p = fma(p, r, 1.0);
@@ -69,12 +77,18 @@ __device__ __forceinline__ double exp_below64(float x, float top)
     return x == top ? 1.0 : exp64(fmax((double)x - (double)top, -800.0));
 }
 
-// floats as unsigned numbers of the same order (0 stays free for "none")
-__device__ __forceinline__ uint32_t order_key(float f)
+// floats as unsigned numbers of the same order; -inf (0x007FFFFF) and 0 below
+// every number
+__device__ __forceinline__ uint32_t order_bits(float f)  // f is not -0
 {
-    const uint32_t u = __float_as_uint(f + 0.0f);  // -0 equals +0
+    const uint32_t u = __float_as_uint(f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t order_key(float f)
+{
+    return order_bits(f + 0.0f);  // -0 equals +0
+}
+constexpr uint32_t kNoKey = 0x007FFFFFu;
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp0(uint32_t v)  // 0 where no lane is read
@@ -168,14 +182,17 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t i)
 template <int PL>
 __device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0, float* x)
 {
-    if (a.wide) {
 #pragma unroll
-        for (int i = 0; i < PL; ++i)
-            x[i] = -__builtin_inff();
-        if (e0 >= a.E)
-            return;
-        if (a.type == W4A8_TYPE_FP32) {
-            const float* p = (const float*)a.logits + row + e0;
+    for (int i = 0; i < PL; ++i)
+        x[i] = -__builtin_inff();
+    if (a.type == W4A8_TYPE_FP32) {
+        const float* p = (const float*)a.logits + row + e0;
+        if (!a.wide) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                if (e0 + i < a.E)
+                    x[i] = p[i];
+        } else if (e0 < a.E) {
             if constexpr (PL >= 4) {
 #pragma unroll
                 for (int i = 0; i < PL; i += 4) {
@@ -188,35 +205,47 @@ __device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0
             } else {
                 x[0] = *p;
             }
-        } else {
-            const uint16_t* p = (const uint16_t*)a.logits + row + e0;
-            uint32_t raw[PL / 2 > 0 ? PL / 2 : 1];
-            if constexpr (PL >= 8) {
-#pragma unroll
-                for (int i = 0; i < PL / 8; ++i) {
-                    const uint4 v = *(const uint4*)(p + 8 * i);
-                    raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
-                }
-            } else if constexpr (PL == 4) {
-                const uint2 v = *(const uint2*)p;
-                raw[0] = v.x, raw[1] = v.y;
-            } else if constexpr (PL == 2) {
-                raw[0] = *(const uint32_t*)p;
-            } else {
-                raw[0] = *p;
-            }
-            const bool bf16 = a.type == W4A8_TYPE_BF16;
-#pragma unroll
-            for (int i = 0; i < PL; ++i) {
-                const uint32_t h = (i & 1) ? raw[i / 2] >> 16 : raw[i / 2] & 0xFFFFu;
-                x[i] = bf16 ? __uint_as_float(h << 16) : half_bits(h);
-            }
         }
         return;
     }
+    constexpr uint32_t kLow = 0xFF80FC00u;  // -inf: bf16 in the high half, fp16 in the low one
+    const uint32_t none = a.type == W4A8_TYPE_BF16 ? kLow >> 16 : kLow & 0xFFFFu;
+    uint32_t raw[(PL + 1) / 2];
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-        x[i] = e0 + i < a.E ? load_logit(a, row + e0 + i) : -__builtin_inff();
+    for (int i = 0; i < (PL + 1) / 2; ++i)
+        raw[i] = none | none << 16;
+    const uint16_t* p = (const uint16_t*)a.logits + row + e0;
+    if (!a.wide) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            if (e0 + i < a.E)
+                raw[i / 2] = (i & 1) ? (raw[i / 2] & 0xFFFFu) | (uint32_t)p[i] << 16
+                                     : (raw[i / 2] & 0xFFFF0000u) | p[i];
+    } else if (e0 < a.E) {
+        if constexpr (PL >= 8) {
+#pragma unroll
+            for (int i = 0; i < PL / 8; ++i) {
+                const uint4 v = *(const uint4*)(p + 8 * i);
+                raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+            }
+        } else if constexpr (PL == 4) {
+            const uint2 v = *(const uint2*)p;
+            raw[0] = v.x, raw[1] = v.y;
+        } else if constexpr (PL == 2) {
+            raw[0] = *(const uint32_t*)p;
+        } else {
+            raw[0] = *p;
+        }
+    }
+    if (a.type == W4A8_TYPE_BF16) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            x[i] = __uint_as_float((i & 1) ? raw[i / 2] & 0xFFFF0000u : raw[i / 2] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            x[i] = half_bits((i & 1) ? raw[i / 2] >> 16 : raw[i / 2] & 0xFFFFu);
+    }
 }
 
 }  // namespace
@@ -224,21 +253,11 @@ __device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0
 // SCORES: the 64-bit scores of all experts are needed (a bias, sums of two per
 // group, or the softmax's whole sum); else the logits alone decide.
 template <int PL, bool SCORES>
-__global__ __launch_bounds__(64 * kRWaves) void route_kernel(const RouteArgs a)
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * kRWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (t >= a.T)
-        return;
     int32_t* const ids = a.ids + t * a.topk;
     float* const wts = a.weights + t * a.topk;
-    if (a.num_tokens != nullptr && t >= *a.num_tokens) {
-        if (lane < a.topk) {
-            ids[lane] = -1;
-            wts[lane] = 0.0f;
-        }
-        return;
-    }
     const int e0 = lane * PL;
     float x[PL];
     load_run<PL>(a, t * a.ld, e0, x);
@@ -285,6 +304,8 @@ __global__ __launch_bounds__(64 * kRWaves) void route_kernel(const RouteArgs a)
                 choice[i] = kNone;
             else if (a.bias != nullptr)
                 key[i] = order_key((float)choice[i]);
+            else if (a.group_top == 1)
+                choice[i] = (double)x[i];  // groups too go by the logits
         }
     } else {
 #pragma unroll
@@ -398,12 +419,339 @@ __global__ __launch_bounds__(64 * kRWaves) void route_kernel(const RouteArgs a)
     if (a.renorm) {
         const double sum = run_sum<0>(s, a.topk);
         s = sum > 0.0 ? s / sum : 0.0;
-    } else if (a.softmax) {
+    } else if (a.softmax && my_id >= 0) {
         s = s / total;
     }
     if (lane < a.topk) {
         ids[lane] = my_id;
         wts[lane] = (float)((double)a.scale * s);
+    }
+}
+
+template <int PL, bool SCORES>
+__global__ __launch_bounds__(64 * kRWaves) void route_kernel(const RouteArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * kRWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (t >= a.T)
+        return;
+    if (a.num_tokens != nullptr && t >= *a.num_tokens) {
+        if (lane < a.topk) {
+            a.ids[t * a.topk + lane] = -1;
+            a.weights[t * a.topk + lane] = 0.0f;
+        }
+        return;
+    }
+    route_token<PL, SCORES>(a, t);
+}
+
+// ---- four tokens per wave ------------------------------------------------------------
+//
+// 16 lanes per token, PL consecutive experts each.  The search runs on keys
+// of 32 bits that carry the expert's slot in their low bits, so each lane
+// sorts its own with a plain min/max network, and a round is a DPP maximum
+// over the row of 16 lanes that leaves the result in all of them; scores are
+// fp32.  That decides every token whose neighbouring choices differ by more
+// than both can be off; the others (about one in 500 of N(0,1) logits with a
+// bias) are done again by route_token, the whole wave on one token.
+
+namespace {
+
+constexpr int kRowK = 8;  // most experts per token here
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v)
+{
+    return __uint_as_float(dpp_u<CTRL>(__float_as_uint(v)));
+}
+constexpr int kRor = 0x120;  // row_ror by n: kRor + n
+
+// the row's maximum in all its lanes
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    v = max(v, dpp_u<kRor + 1>(v));
+    v = max(v, dpp_u<kRor + 2>(v));
+    v = max(v, dpp_u<kRor + 4>(v));
+    return max(v, dpp_u<kRor + 8>(v));
+}
+__device__ __forceinline__ float row_sum16(float v)
+{
+    v += dpp_f<kRor + 1>(v);
+    v += dpp_f<kRor + 2>(v);
+    v += dpp_f<kRor + 4>(v);
+    return v + dpp_f<kRor + 8>(v);
+}
+__device__ __forceinline__ float key_value(uint32_t key)
+{
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+// descending, by odd-even merges
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[N])
+{
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t hi = max(v[i + j], v[i + j + k]);
+                        v[i + j + k] = min(v[i + j], v[i + j + k]);
+                        v[i + j] = hi;
+                    }
+}
+
+// other groups of the row, one rotation after another: how many are better
+// than this lane's, and whether any is too close to tell
+template <int N>
+__device__ __forceinline__ void rank_groups(float mine, int group, int run, float slack, int& better, bool& close)
+{
+    if constexpr (N < 16) {
+        if ((N & (run - 1)) == 0) {
+            const float v = dpp_f<kRor + N>(mine);
+            const int g = (int)dpp_u<kRor + N>((uint32_t)group);
+            better += (v > mine || (v == mine && g < group)) ? 1 : 0;
+            // two equal infinities (false here) tie in 64 bits too
+            close |= fabsf(v - mine) <= slack + dpp_f<kRor + N>(slack);
+        }
+        rank_groups<N + 1>(mine, group, run, slack, better, close);
+    }
+}
+
+}  // namespace
+
+// What orders the experts: their choice in fp32 (with a bias), or their logits
+// (without), exactly for the 16-bit types, whose keys hold the index too (they
+// leave the low 13 or 16 bits of a float free).
+enum RowKey { KEY_CHOICE, KEY_LOGIT32, KEY_LOGIT16 };
+
+template <int PL, int KEY>
+__global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
+{
+    constexpr uint32_t kSlots = 15;  // low bits of a key: 15 - slot
+    const float ninf = -__builtin_inff();
+    const int lane = threadIdx.x & 63, l = lane & 15;
+    const int waves = (int)blockDim.x >> 6;
+    const int64_t t0 =
+        ((int64_t)blockIdx.x * waves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 4;
+    if (t0 >= a.T)
+        return;
+    int64_t valid = a.T;  // rows from here on are padding
+    if (a.num_tokens != nullptr)
+        valid = min(valid, (int64_t)*a.num_tokens);
+    const int64_t t = t0 + (lane >> 4);
+    const bool live = t < valid;
+    const int64_t row = (live ? t : t0) * a.ld;
+
+    const int e0 = l * PL;
+    float x[PL];
+    if (live) {
+        load_run<PL>(a, row, e0, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            x[i] = ninf;
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+        x[i] = fmaxf(x[i], ninf);  // NaN: -inf, which is what cannot be chosen
+    float top = ninf;
+    double total = 1.0;  // of the softmax, where the weights need it
+    if (a.softmax) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            top = fmaxf(top, x[i]);
+        top = fmaxf(top, dpp_f<kRor + 1>(top));
+        top = fmaxf(top, dpp_f<kRor + 2>(top));
+        top = fmaxf(top, dpp_f<kRor + 4>(top));
+        top = fmaxf(top, dpp_f<kRor + 8>(top));
+        if (!a.renorm) {
+            total = 0.0;
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                total += x[i] > ninf ? exp_below64(x[i], top) : 0.0;
+            total = run_sum<0>(total, 16);
+        }
+    }
+    // choices in fp32, off by at most `off` + 2^-23 of their value: the
+    // sigmoid's product, exp2, sum and reciprocal cost 2^-22 (kept: 2^-21), the
+    // softmax's sum of up to 20 roundings 2^-19.7 of its terms
+    const bool sums = a.groups > 1 && a.group_top == 2;
+    const float off = a.softmax ? 0x1p-19f : 0x1p-21f;
+    uint32_t key[PL], gkey[PL];  // of the experts' order, and of the groups'
+    if (KEY == KEY_CHOICE || sums) {
+        float c[PL];
+        if (a.softmax) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                c[i] = x[i] == top ? 1.0f : __builtin_amdgcn_exp2f((x[i] - top) * 1.44269504f);
+                sum += c[i];
+            }
+            const float inv = __builtin_amdgcn_rcpf(row_sum16(sum));
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                c[i] *= inv;
+        } else {
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x[i] * -1.44269504f));
+        }
+        float b[PL];  // small enough for the L1; loaded here to hold fewer registers
+        if (KEY == KEY_CHOICE) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                b[i] = 0.0f;
+            if (a.E % PL == 0) {
+                if (e0 < a.E) {
+#pragma unroll
+                    for (int i = 0; i < PL; i += 4) {
+                        const float4 v = *(const float4*)(a.bias + e0 + i);
+                        b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PL; ++i)
+                    if (e0 + i < a.E)
+                        b[i] = a.bias[e0 + i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            if (KEY == KEY_CHOICE)
+                c[i] = fmaxf(c[i] + b[i], ninf);  // a NaN bias: -inf
+            gkey[i] = x[i] > ninf ? order_bits(c[i]) : kNoKey;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        if (KEY == KEY_CHOICE) {
+            key[i] = gkey[i];
+        } else {
+            key[i] = order_key(x[i]);
+            if (!sums)
+                gkey[i] = key[i];
+        }
+    }
+    bool close = false;  // some pair of the row is too close for 32 bits
+    bool open = true;    // the lane's group stays
+    if (a.groups > 1) {
+        const int run = a.E / a.groups / PL;  // lanes of a group, a power of two
+        uint32_t b1 = gkey[0], b2 = kNoKey;
+#pragma unroll
+        for (int i = 1; i < PL; ++i) {
+            b2 = max(b2, min(b1, gkey[i]));
+            b1 = max(b1, gkey[i]);
+        }
+        auto merge = [&](uint32_t c1, uint32_t c2) {
+            b2 = max(max(b2, c2), min(b1, c1));
+            b1 = max(b1, c1);
+        };
+        if (run > 1)
+            merge(dpp_u<kXor1>(b1), dpp_u<kXor1>(b2));
+        if (run > 2)
+            merge(dpp_u<kXor2>(b1), dpp_u<kXor2>(b2));
+        if (run > 4)
+            merge(dpp_u<kHalfMirror>(b1), dpp_u<kHalfMirror>(b2));
+        const float v1 = key_value(b1), v2 = key_value(b2);
+        const bool two = sums && b2 > kNoKey;
+        // logits compare exactly; a sum is off by as much as both its terms,
+        // whose magnitudes count where they cancel
+        float slack = -1.0f;
+        if (KEY == KEY_CHOICE || sums)
+            slack = 2.0f * off + 0x1p-22f * (fabsf(v1) + (two ? fabsf(v2) : 0.0f));
+        int better = 0;
+        rank_groups<1>(two ? v1 + v2 : v1, l / run, run, slack, better, close);
+        open = better < a.kept;
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+        key[i] = KEY == KEY_LOGIT16 ? (key[i] & ~0xFFu) | (uint32_t)(0xFF - e0 - i)
+                                    : (key[i] & ~kSlots) | (uint32_t)(kSlots - i);
+    sort_down(key);
+    key[0] = open ? key[0] : 0;  // this lane never holds the largest
+    uint32_t mine = 0, lanes_lo = 0, lanes_hi = 0;  // lane j: key j, and which lanes held it
+#pragma unroll
+    for (int j = 0; j < kRowK; ++j) {
+        if (j == a.topk)
+            break;
+        const uint32_t m = row_max(key[0]);
+        const bool won = key[0] == m;
+        const uint64_t lanes = __ballot(won);
+        mine = l == j ? m : mine;
+        lanes_lo = l == j ? (uint32_t)lanes : lanes_lo;
+        lanes_hi = l == j ? (uint32_t)(lanes >> 32) : lanes_hi;
+#pragma unroll
+        for (int i = 0; i < kRowK - j && i < PL; ++i)
+            key[i] = won ? (i + 1 < PL ? key[i + 1] : 0) : key[i];
+    }
+    const uint32_t rest = row_max(key[0]);  // the best that is not chosen
+    mine = l == a.topk ? rest : mine;
+    const uint32_t next = dpp_u<0x101>(mine);  // row_shl: of lane l + 1
+    const bool chosen = l < a.topk && mine > kNoKey;
+    bool near = false;  // too close to the next one for the keys to tell
+    if (KEY != KEY_LOGIT16 && chosen && next > kNoKey) {
+        if (KEY == KEY_CHOICE) {
+            // both off by `off` + 2^-23 and 15 steps of 2^-23 for the slot
+            const float v = key_value(mine), w = key_value(next);
+            near = !(v - w > 2.0f * off + 0x1p-18f * (fabsf(v) + fabsf(w)));
+        } else {
+            near = ((mine ^ next) & ~kSlots) == 0;
+        }
+    }
+    int my_id = -1;
+    double s = 0.0, exact = kNone;
+    if (chosen) {
+        const uint32_t lanes = ((lane & 32 ? lanes_hi : lanes_lo) >> (lane & 16)) & 0xFFFF;
+        my_id = KEY == KEY_LOGIT16 ? (int)(0xFF - (mine & 0xFF))
+                                   : (__ffs((int)lanes) - 1) * PL + (int)(kSlots - (mine & kSlots));
+        close |= KEY != KEY_LOGIT16 && (lanes & (lanes - 1)) != 0;  // one key in several lanes: all gave it up
+        const float v = load_logit(a, row + my_id);
+        s = a.softmax ? exp_below64(v, top) : sigmoid64(v);
+        exact = (double)v;
+    }
+    if (KEY != KEY_LOGIT16 && __ballot(near) != 0) {
+        // two chosen ones that 64 bits find in order are fine; the last chosen
+        // one against all the others is not known that way
+        if (KEY == KEY_CHOICE && chosen)
+            exact = s + (double)a.bias[my_id];
+        const double other = dpp_d<0x101>(exact);
+        const int other_id = (int)dpp_u<0x101>((uint32_t)my_id);
+        const bool ordered = l + 1 < a.topk && (KEY == KEY_LOGIT32 || !a.softmax) &&
+                             (exact > other || (exact == other && my_id < other_id));
+        close |= near && !ordered;
+    }
+    if (a.renorm) {
+        const double sum = run_sum<0>(s, a.topk);
+        s = sum > 0.0 ? s / sum : 0.0;
+    } else if (a.softmax && chosen) {
+        s = s / total;
+    }
+    const uint64_t again = KEY != KEY_LOGIT16 || sums ? __ballot(close && live) : 0;
+    if (t < a.T && l < a.topk && ((again >> (lane & 48)) & 0xFFFF) == 0) {
+        a.ids[t * a.topk + l] = my_id;
+        a.weights[t * a.topk + l] = (float)((double)a.scale * s);
+    }
+    if (again != 0) {
+        for (int r = 0; r < 4; ++r)
+            if ((again >> (16 * r)) & 0xFFFF) {
+                if (PL == 4)
+                    route_token<1, true>(a, t0 + r);
+                else if (PL == 8)
+                    route_token<2, true>(a, t0 + r);
+                else
+                    route_token<4, true>(a, t0 + r);
+            }
     }
 }
 
@@ -424,8 +772,48 @@ void launch_lanes(const RouteArgs& a, bool scores, hipStream_t s)
 
 }  // namespace
 
+namespace {
+
+// rows of 16 lanes: up to 8 of up to 256 experts, groups that are runs of
+// 1, 2, 4 or 8 lanes
+template <int PL>
+bool row_groups(const RouteArgs& a)
+{
+    const int size = a.E / a.groups, run = size / PL;
+    return a.groups == 1 || (run * PL == size && run >= 1 && run <= 8 && (run & (run - 1)) == 0);
+}
+template <int PL>
+void launch_rows(const RouteArgs& a, hipStream_t s)
+{
+    RouteArgs b = a;
+    b.wide = (a.ld * (a.type == W4A8_TYPE_FP32 ? 4 : 2)) % 16 == 0 && a.E % PL == 0;
+    // few tokens: a wave per workgroup, so that they spread over the CUs
+    const int waves = a.T <= 4096 ? 1 : 4;
+    const dim3 grid((unsigned)((a.T + 4 * waves - 1) / (4 * waves))), block(64 * waves);
+    if (a.bias != nullptr)
+        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_CHOICE>), grid, block, 0, s, b);
+    else if (a.type == W4A8_TYPE_FP32)
+        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_LOGIT32>), grid, block, 0, s, b);
+    else
+        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_LOGIT16>), grid, block, 0, s, b);
+}
+
+}  // namespace
+
 hipError_t launch_route(const RouteArgs& a, hipStream_t s)
 {
+    if (a.topk <= kRowK && a.E <= 256) {
+        const bool p4 = a.E <= 64, p8 = a.E <= 128;
+        if (p4 ? row_groups<4>(a) : p8 ? row_groups<8>(a) : row_groups<16>(a)) {
+            if (p4)
+                launch_rows<4>(a, s);
+            else if (p8)
+                launch_rows<8>(a, s);
+            else
+                launch_rows<16>(a, s);
+            return hipGetLastError();
+        }
+    }
     const bool scores =
         a.bias != nullptr || (a.groups > 1 && a.group_top == 2) || (a.softmax && !a.renorm);
     if (a.E <= 64)
