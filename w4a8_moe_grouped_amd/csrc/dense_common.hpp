@@ -1,0 +1,101 @@
+// dense_common.hpp -- what the kernels of w4a8_gemm_epilogue share: the int4
+// decode and the epilogue of four consecutive outputs.
+#pragma once
+
+#include "w4a8.h"
+
+#include "common.hpp"
+#include "internal.hpp"
+
+namespace w4a8 {
+
+// four nibbles (one per byte, two's complement) -> e4m3 codes of v * 2^-9:
+// |v| <= 7 are the subnormal codes |v|, 8 is code 0x08
+__device__ __forceinline__ uint32_t nibbles_to_e4m3(uint32_t b)
+{
+    const uint32_t s = (b >> 3) & 0x01010101u;  // sign per byte
+    const uint32_t m = s * 0x0Fu;
+    return ((b ^ m) + s) | (s << 7);
+}
+
+// 16 packed bytes (32 nibbles, k even in the low nibble) -> 32 e4m3 codes in
+// natural K order
+__device__ __forceinline__ v8i int4_to_fp8(const v4i& w)
+{
+    v8i r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = (uint32_t)w[i];
+        const uint32_t lo = nibbles_to_e4m3(x & 0x0F0F0F0Fu);         // k0, k2, k4, k6
+        const uint32_t hi = nibbles_to_e4m3((x >> 4) & 0x0F0F0F0Fu);  // k1, k3, k5, k7
+        r[2 * i] = (int)__builtin_amdgcn_perm(hi, lo, 0x05010400u);
+        r[2 * i + 1] = (int)__builtin_amdgcn_perm(hi, lo, 0x07030602u);
+    }
+    return r;
+}
+
+__device__ __forceinline__ float load_bias(const DenseArgs& a, int64_t n)
+{
+    return a.bias_bf16 ? bf16_to_f32(((const uint16_t*)a.bias)[n]) : ((const float*)a.bias)[n];
+}
+
+__device__ __forceinline__ float silu(float y)
+{
+    return y / (1.0f + expf(-y));
+}
+
+// act of one value (not SwiGLU); the forms with the tail as a product keep
+// small results where 1 + erf and 1 + tanh cancel
+__device__ __forceinline__ float activate(float y, int act)
+{
+    switch (act) {
+    case W4A8_ACT_RELU: return y < 0.0f ? 0.0f : y;  // NaN stays
+    case W4A8_ACT_SILU: return silu(y);
+    case W4A8_ACT_GELU: return 0.5f * y * erfcf(-0.70710678118654752f * y);
+    case W4A8_ACT_GELU_TANH: {
+        const float u = 0.79788456080286536f * fmaf(0.044715f * y * y, y, y);
+        return y / (1.0f + expf(-2.0f * u));
+    }
+    default: return y;
+    }
+}
+
+// four consecutive outputs n0.. of row m: y their sums (up: the up rows' sums
+// with SwiGLU), then bias, activation, residual and the one rounding
+__device__ __forceinline__ void epilogue4(const DenseArgs& a, int64_t m, int64_t n0, const float* y,
+                                          const float* up)
+{
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t n = n0 + i < a.N ? n0 + i : a.N - 1;
+        const float b = a.bias != nullptr ? load_bias(a, n) : 0.0f;
+        if (a.act == W4A8_ACT_SWIGLU)
+            o[i] = silu(y[i] + b) * (up[i] + (a.bias != nullptr ? load_bias(a, a.N + n) : 0.0f));
+        else
+            o[i] = activate(y[i] + b, a.act);
+    }
+    if (a.vec4) {  // N % 4 == 0: all four are inside
+        if (n0 >= a.N)
+            return;
+        if (a.residual != nullptr) {
+            const uint2 r = *(const uint2*)(a.residual + m * a.ldr + n0);
+            o[0] += __uint_as_float(r.x << 16);
+            o[1] += __uint_as_float(r.x & 0xFFFF0000u);
+            o[2] += __uint_as_float(r.y << 16);
+            o[3] += __uint_as_float(r.y & 0xFFFF0000u);
+        }
+        *(uint2*)(a.out + m * a.ldo + n0) = make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n0 + i >= a.N)
+            return;
+        if (a.residual != nullptr)
+            o[i] += bf16_to_f32(a.residual[m * a.ldr + n0 + i]);
+        a.out[m * a.ldo + n0 + i] = (uint16_t)f32x2_to_bf16x2(o[i], 0.0f);
+    }
+}
+
+}  // namespace w4a8

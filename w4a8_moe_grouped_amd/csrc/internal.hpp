@@ -261,5 +261,10 @@ struct DenseArgs {
 };
 size_t dense_epilogue_workspace(int64_t M, int64_t K, int64_t N, int act);
 hipError_t launch_dense_epilogue(const DenseArgs& a, void* ws, hipStream_t s);
+// many rows (dense_tiles.hip): from which sizes on, and the workspace of its
+// expanded weights
+bool use_dense_tiles(int64_t M, int64_t K, int64_t N, int act);
+size_t dense_tiles_workspace(int64_t M, int64_t K, int64_t N, int act);
+hipError_t launch_dense_tiles(const DenseArgs& a, void* ws, hipStream_t s);
 
 } // namespace w4a8
