@@ -164,6 +164,14 @@ __global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
             for (int i = 0; i < 4; ++i)
                 acc[s][f][i] = 0.0f;
 
+    // LDS offsets of the lane's operands in a stage; slice s and fragment f lie
+    // at constant distances (16 rows do not change the swizzle)
+    const uint32_t oa0 = 16 * slot(BM / 2 * wm + c16, q), oa1 = 16 * slot(BM / 2 * wm + c16, 4 + q);
+    const uint32_t ob0 = kAStage + 16 * slot(64 * wn + c16, q), ob1 = kAStage + 16 * slot(64 * wn + c16, 4 + q);
+    const uint32_t osw = kAStage + kWStage + 4 * (64 * wn + 4 * q);
+    const uint32_t osa = kAStage + kWStage + kScaleStage + 4 * (BM / 2 * wm + c16);
+    constexpr int kFrag = 16 * kGroup;  // bytes of 16 rows
+
     issue(0, 0);
     for (int g = 0; g < G; ++g) {
         wait_vmcnt<0>();
@@ -171,31 +179,63 @@ __global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
         if (g + 1 < G)
             issue(g + 1, (g + 1) & 1);
         const uint8_t* st = smem + (g & 1) * kStage;
+        const uint8_t *pa0 = st + oa0, *pa1 = st + oa1, *pb0 = st + ob0, *pb1 = st + ob1;
+        const uint8_t *psw = st + osw, *psa = st + osa;
+        auto read = [&](const uint8_t* p0, const uint8_t* p1, int i) {
+            const v4i x0 = *(const v4i*)(p0 + i * kFrag), x1 = *(const v4i*)(p1 + i * kFrag);
+            return v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+        };
+        v8i av = read(pa0, pa1, 0);
         v8i b[4];
         float4 sw[4];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const int r = 64 * wn + 16 * f + c16;
-            const v4i b0 = *(const v4i*)(st + kAStage + 16 * slot(r, 2 * q));
-            const v4i b1 = *(const v4i*)(st + kAStage + 16 * slot(r, 2 * q + 1));
-            b[f] = v8i{b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
-            sw[f] = *(const float4*)(st + kAStage + kWStage + 4 * (64 * wn + 16 * f + 4 * q));
-        }
+        for (int f = 0; f < 4; ++f)
+            b[f] = read(pb0, pb1, f);
+        float sa = *(const float*)psa;
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+            sw[f] = *(const float4*)(psw + 64 * f);
+        // slice s is multiplied while slice s - 1 gets its scales: the vector
+        // unit works on results that are already there
+        v4f raw[4];
+        float sa_raw = 0.0f;  // scale of the rows in raw
+        auto promote = [&](int s, int f) {
+            acc[s][f][0] = fmaf(sw[f].x, raw[f][0] * sa_raw, acc[s][f][0]);
+            acc[s][f][1] = fmaf(sw[f].y, raw[f][1] * sa_raw, acc[s][f][1]);
+            acc[s][f][2] = fmaf(sw[f].z, raw[f][2] * sa_raw, acc[s][f][2]);
+            acc[s][f][3] = fmaf(sw[f].w, raw[f][3] * sa_raw, acc[s][f][3]);
+        };
 #pragma unroll
         for (int s = 0; s < kSl; ++s) {
-            const int r = BM / 2 * wm + 16 * s + c16;
-            const v4i a0 = *(const v4i*)(st + 16 * slot(r, 2 * q));
-            const v4i a1 = *(const v4i*)(st + 16 * slot(r, 2 * q + 1));
-            const float sa = *(const float*)(st + kAStage + kWStage + kScaleStage + 4 * r);
-            const v8i av = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
+            v8i next = av;
+            float sa_next = sa;
+            if (s + 1 < kSl) {
+                next = read(pa0, pa1, s + 1);
+                sa_next = *(const float*)(psa + 64 * (s + 1));
+            }
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
-                const v4f raw = mfma16x16x128(b[f], av, v4f{0.0f, 0.0f, 0.0f, 0.0f});
-                acc[s][f][0] = fmaf(sw[f].x, raw[0] * sa, acc[s][f][0]);
-                acc[s][f][1] = fmaf(sw[f].y, raw[1] * sa, acc[s][f][1]);
-                acc[s][f][2] = fmaf(sw[f].z, raw[2] * sa, acc[s][f][2]);
-                acc[s][f][3] = fmaf(sw[f].w, raw[3] * sa, acc[s][f][3]);
+                const v4f r = mfma16x16x128(b[f], av, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+                if (s > 0)
+                    promote(s - 1, f);
+                raw[f] = r;
             }
+            sa_raw = sa;
+            av = next;
+            sa = sa_next;
+        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+            promote(kSl - 1, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // the first slice's MFMAs
+#pragma unroll
+        for (int i = 0; i < 4 * (kSl - 1); ++i) {
+            if (i % 4 == 0)
+                __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);  // the next slice's reads
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // one MFMA
+            __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);      // one promotion
         }
     }
     // Epilogue: each wave lays 64 of its rows at a time into its own part of
