@@ -533,8 +533,8 @@ int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* resid
  *   workspace    device scratch of *workspace_bytes bytes (query with NULL; it
  *                depends on M, K, N and activation alone, and may be 0)
  * M >= 0 (M == 0 launches nothing), N > 0, K > 0 (INVALID_ARG otherwise), K %
- * 128 == 0, K <= 2^22, M, R < 2^31, pointers 16-byte aligned (UNSUPPORTED
- * otherwise).  Operands may exceed 2^32 bytes.
+ * 128 == 0, K <= 2^22, M, R < 2^31, ceil(M/32) * ceil(N/16) < 2^31, pointers
+ * 16-byte aligned (UNSUPPORTED otherwise).  Operands may exceed 2^32 bytes.
  */
 #define W4A8_ACT_NONE 0
 #define W4A8_ACT_RELU 1

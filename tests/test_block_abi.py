@@ -77,6 +77,7 @@ def _gemm(L, a=P, sa=P, M=0, K=256, b=P, sb=P, N=64, bias=None, bt=0, act=0, res
     (dict(), OK), (dict(M=-1), INVALID), (dict(K=0), INVALID), (dict(N=0), INVALID), (dict(act=6), INVALID),
     (dict(act=-1), INVALID), (dict(K=200), UNSUPPORTED), (dict(K=(1 << 22) + 128), UNSUPPORTED),
     (dict(M=1 << 31), UNSUPPORTED), (dict(N=1 << 31), UNSUPPORTED), (dict(N=1 << 30, act=5), UNSUPPORTED),
+    (dict(M=1 << 30, N=1 << 11, ldo=1 << 11), UNSUPPORTED),
     (dict(M=4, a=None), INVALID), (dict(M=4, sa=None), INVALID), (dict(b=None), INVALID), (dict(sb=None), INVALID),
     (dict(M=4, out=None), INVALID), (dict(ldo=63), INVALID), (dict(res=P, ldr=63), INVALID),
     (dict(bias=P, bt=2), INVALID), (dict(res=P2, ldr=72), INVALID), (dict(M=4, a=ODD), UNSUPPORTED),

@@ -357,6 +357,43 @@ def test_gemm_epilogue(dev, M, K, N, act):
     check_gemm(ops, activation=act, bias=bias.to(BF16))
 
 
+# sizes that run on tiles: whole ones, and ones whose last tiles hold one row,
+# one column, half a unit; one and several groups
+@pytest.mark.parametrize("M, K, N, act", [
+    (4096, 128, 4096, "none"), (4097, 256, 4001, "silu"), (4001, 384, 2050, "swiglu"), (2000, 1152, 4097, "gelu"),
+    (8000, 256, 1000, "relu"), (3000, 1024, 3001, "none"), (2570, 2048, 2049, "swiglu"), (2100, 7168, 4096, "none"),
+    (2500, 640, 4230, "gelu_tanh")])
+def test_gemm_epilogue_tiles(dev, M, K, N, act):
+    assert w4.gemm_epilogue_workspace_bytes(M, K, N, act) > 0
+    R = 2 * N if act == "swiglu" else N
+    ops = gemm_inputs(dev, M, K, R)
+    g = gen(dev, 98)
+    bias = torch.randn(R, generator=g, device=dev)
+    res = torch.randn(M, N, generator=g, device=dev).to(BF16)
+    check_gemm(ops, activation=act, bias=bias, residual=res)
+    # a workspace full of NaN, a row stride, the residual updated in place
+    ws = torch.full((w4.gemm_epilogue_workspace_bytes(M, K, N, act),), 0xFF, dtype=torch.uint8, device=dev)
+    rr = padded(res, 5)
+    check_gemm(ops, activation=act, residual=res,
+               got=w4.gemm_epilogue(*ops, activation=act, residual=rr, out=rr, workspace=ws))
+    with pytest.raises(w4.W4A8Error):
+        w4.gemm_epilogue(*ops, activation=act, workspace=ws[:-16])
+
+
+def test_gemm_epilogue_tiles_same_sign_and_extremes(dev):
+    q, s, w, sw = ops = gemm_inputs(dev, 4096, 256, 4096, dist="positive")
+    assert w4.gemm_epilogue_workspace_bytes(4096, 256, 4096) > 0
+    check_gemm(ops)
+    check_gemm((torch.full_like(q, 0x7E), s, torch.full_like(w, 0x88), sw))
+    s2, sw2 = s.clone(), sw.clone()
+    s2[300, 1], sw2[9, 0] = math.nan, INF
+    want, got = w4.gemm_epilogue(*ops), w4.gemm_epilogue(q, s2, w, sw2)
+    assert bool(torch.isnan(got[300]).all()) and not bool(torch.isfinite(got[:, 9]).any())
+    keep = torch.ones(4096, 4096, dtype=torch.bool, device=dev)
+    keep[300], keep[:, 9] = False, False
+    assert torch.equal(got[keep], want[keep])
+
+
 @pytest.mark.parametrize("M", [1, 40, 300, 600])
 def test_gemm_epilogue_same_sign_and_extremes(dev, M):
     """Sums that do not cancel; codes of +-448; weights of -8 everywhere."""

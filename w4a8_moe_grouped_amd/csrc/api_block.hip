@@ -149,6 +149,9 @@ int w4a8_gemm_epilogue(const uint8_t* a_e4m3, const float* a_scales, int64_t M, 
     if (K % W4A8_GROUP != 0 || K > kMaxDenseK || M > INT32_MAX ||
         mul_sat(N, activation == W4A8_ACT_SWIGLU ? 2 : 1) > INT32_MAX)
         return W4A8_ERR_UNSUPPORTED;
+    // workgroups of 32 rows x at least 16 outputs
+    if (mul_sat(ceil_div(M, 32), ceil_div(N, 16)) > INT32_MAX)
+        return W4A8_ERR_UNSUPPORTED;
     const size_t need = w4a8::dense_epilogue_workspace(M, K, N, activation);
     const int ws_rc = check_workspace(workspace, workspace_bytes, need);
     if (ws_rc >= 0)
@@ -181,6 +184,7 @@ int w4a8_gemm_epilogue(const uint8_t* a_e4m3, const float* a_scales, int64_t M, 
     d.out = (uint16_t*)out_bf16;
     d.ldo = ld_out;
     d.vec4 = N % 4 == 0 && ld_out % 4 == 0 && (residual_bf16 == nullptr || ld_residual % 4 == 0);
+    d.vec2 = N % 2 == 0 && ld_out % 2 == 0 && (residual_bf16 == nullptr || ld_residual % 2 == 0);
     return hip_status(w4a8::launch_dense_epilogue(d, workspace, stream));
 }
 

@@ -60,32 +60,75 @@ __device__ __forceinline__ float activate(float y, int act)
     }
 }
 
+// What the epilogue of four outputs reads, loaded ahead of the sums.
+struct EpiOperands {
+    uint2 residual;  // four bf16 (vec4 and vec2)
+    float bias[4], bias_up[4];
+};
+__device__ __forceinline__ EpiOperands load_epilogue4(const DenseArgs& a, int64_t m, int64_t n0)
+{
+    EpiOperands e = {};
+    if (a.residual != nullptr && n0 < a.N) {
+        const uint16_t* r = a.residual + m * a.ldr + n0;
+        if (a.vec4) {
+            e.residual = *(const uint2*)r;
+        } else if (a.vec2) {
+            e.residual.x = *(const uint32_t*)r;
+            if (n0 + 2 < a.N)
+                e.residual.y = *(const uint32_t*)(r + 2);
+        }
+    }
+    if (a.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t n = n0 + i < a.N ? n0 + i : a.N - 1;
+            e.bias[i] = load_bias(a, n);
+            if (a.act == W4A8_ACT_SWIGLU)
+                e.bias_up[i] = load_bias(a, a.N + n);
+        }
+    }
+    return e;
+}
+
 // four consecutive outputs n0.. of row m: y their sums (up: the up rows' sums
 // with SwiGLU), then bias, activation, residual and the one rounding
 __device__ __forceinline__ void epilogue4(const DenseArgs& a, int64_t m, int64_t n0, const float* y,
-                                          const float* up)
+                                          const float* up, const EpiOperands& e)
 {
     float o[4];
+    if (a.act == W4A8_ACT_SWIGLU) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t n = n0 + i < a.N ? n0 + i : a.N - 1;
-        const float b = a.bias != nullptr ? load_bias(a, n) : 0.0f;
-        if (a.act == W4A8_ACT_SWIGLU)
-            o[i] = silu(y[i] + b) * (up[i] + (a.bias != nullptr ? load_bias(a, a.N + n) : 0.0f));
-        else
-            o[i] = activate(y[i] + b, a.act);
+        for (int i = 0; i < 4; ++i)
+            o[i] = silu(y[i] + e.bias[i]) * (up[i] + e.bias_up[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = a.act == W4A8_ACT_NONE ? y[i] + e.bias[i] : activate(y[i] + e.bias[i], a.act);
     }
     if (a.vec4) {  // N % 4 == 0: all four are inside
         if (n0 >= a.N)
             return;
         if (a.residual != nullptr) {
-            const uint2 r = *(const uint2*)(a.residual + m * a.ldr + n0);
-            o[0] += __uint_as_float(r.x << 16);
-            o[1] += __uint_as_float(r.x & 0xFFFF0000u);
-            o[2] += __uint_as_float(r.y << 16);
-            o[3] += __uint_as_float(r.y & 0xFFFF0000u);
+            o[0] += __uint_as_float(e.residual.x << 16);
+            o[1] += __uint_as_float(e.residual.x & 0xFFFF0000u);
+            o[2] += __uint_as_float(e.residual.y << 16);
+            o[3] += __uint_as_float(e.residual.y & 0xFFFF0000u);
         }
         *(uint2*)(a.out + m * a.ldo + n0) = make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
+        return;
+    }
+    if (a.vec2) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            if (n0 + i >= a.N)
+                return;
+            if (a.residual != nullptr) {
+                const uint32_t r = i == 0 ? e.residual.x : e.residual.y;
+                o[i] += __uint_as_float(r << 16);
+                o[i + 1] += __uint_as_float(r & 0xFFFF0000u);
+            }
+            *(uint32_t*)(a.out + m * a.ldo + n0 + i) = f32x2_to_bf16x2(o[i], o[i + 1]);
+        }
         return;
     }
 #pragma unroll

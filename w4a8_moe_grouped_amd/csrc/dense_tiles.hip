@@ -23,16 +23,20 @@
 #include "dense_common.hpp"
 #include "lds_direct.hpp"
 
+#include <math.h>
+
 namespace w4a8 {
 
 namespace {
 
-constexpr int kBN = 256;                 // weight rows per tile
-constexpr int kWStage = kBN * kGroup;    // 32 KB of codes
-constexpr int kScaleStage = 1024;        // 256 floats
+// Operands are laid out in units of 128 rows: a unit's codes of one group are
+// 16 KB, its scales 512 bytes.
+constexpr int kUnit = 128;
+constexpr int kUnitCodes = kUnit * kGroup;
+constexpr int kUnitScales = kUnit * 4;
 
-// 16-byte slot of (row, chunk 0..7 of its 128 bytes): the XOR spreads a
-// column of chunks over the banks
+// 16-byte slot of (row, chunk 0..7 of its 128 bytes): the XOR spreads what the
+// lanes of one LDS cycle read (8 rows, two neighbouring chunks) over the banks
 __device__ __forceinline__ int slot(int row, int chunk)
 {
     return row * 8 + (chunk ^ (row & 7));
@@ -40,98 +44,140 @@ __device__ __forceinline__ int slot(int row, int chunk)
 
 struct TileArgs {
     DenseArgs d;
-    uint8_t* wq;  // [tiles_n][G][32 KB]
-    float* swt;   // [tiles_n][G][256]
-    float* sat;   // [tiles_m][G][256] (BM of them used)
-    int32_t G, tiles_m, tiles_n, bm;
+    uint8_t* wq;  // [units_n][G][16 KB]
+    float* swt;   // [units_n][G][128]
+    float* sat;   // [units_m][G][128]
+    int32_t G, units_m, units_n;
 };
 
-// weight row of row r of column tile tn (clamped into the matrix)
-__device__ __forceinline__ int64_t tile_weight_row(const DenseArgs& d, int64_t tn, int r)
+// weight row of row r of unit u (clamped into the matrix); SwiGLU: 32 gate
+// rows, their 32 up rows, and so on
+__device__ __forceinline__ int64_t unit_weight_row(const DenseArgs& d, int64_t u, int r)
 {
     if (d.act == W4A8_ACT_SWIGLU) {
-        const int64_t n = tn * (kBN / 2) + (r >> 6) * 32 + (r & 31);
+        const int64_t n = u * (kUnit / 2) + (r >> 6) * 32 + (r & 31);
         return (r & 32 ? d.N : 0) + min(n, d.N - 1);
     }
-    return min(tn * kBN + r, d.N - 1);
+    return min(u * kUnit + r, d.N - 1);
 }
 
 }  // namespace
 
-// Blocks [0, tiles_n * ceil(G/2)): two groups of one column tile; then
-// tiles_m * ceil(G/8) blocks: eight groups of activation scales of one row
-// tile.
+// Blocks [0, units_n * ceil(G/2)): two groups (a row's 128 bytes) of one unit
+// of weights; then units_m * ceil(G/8) blocks: eight groups of activation
+// scales of one unit of rows.
 __global__ __launch_bounds__(256) void dense_expand_kernel(const TileArgs t)
 {
     const DenseArgs& d = t.d;
     const int tid = threadIdx.x;
-    const int64_t pairs = (t.G + 1) / 2;
+    const int pairs = (t.G + 1) / 2;
     int64_t b = blockIdx.x;
-    if (b < t.tiles_n * pairs) {
-        const int64_t tn = b / pairs;
-        const int g0 = 2 * (int)(b - tn * pairs);
-        const int ng = min(2, t.G - g0);
+    if (b < (int64_t)t.units_n * pairs) {
+        const int64_t u = (int)blockIdx.x / pairs;
+        const int g0 = 2 * ((int)blockIdx.x - (int)u * pairs);
         // 16 packed bytes an item: eight of one row lie in one 128-byte line
-#pragma unroll 4
-        for (int i = 0; i < 8; ++i) {
-            const int item = i * 256 + tid;
-            const int r = item >> 3, g = (item >> 2) & 1, q = item & 3;
-            if (g >= ng)
-                continue;
-            const int64_t n = tile_weight_row(d, tn, r);
-            const v8i c = int4_to_fp8(ldg16_nt(d.w + n * (d.K / 2) + (int64_t)(g0 + g) * (kGroup / 2) + 16 * q));
-            uint8_t* dst = t.wq + (tn * t.G + g0 + g) * kWStage;
-            *(v4i*)(dst + 16 * slot(r, 2 * q)) = v4i{c[0], c[1], c[2], c[3]};
-            *(v4i*)(dst + 16 * slot(r, 2 * q + 1)) = v4i{c[4], c[5], c[6], c[7]};
+        const int g = (tid >> 2) & 1, q = tid & 3;
+        const bool in = g0 + g < t.G;
+        v4i w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t n = unit_weight_row(d, u, 32 * i + (tid >> 3));
+            w[i] = ldg16_nt(d.w + n * (d.K / 2) + (int64_t)(in ? g0 + g : g0) * (kGroup / 2) + 16 * q);
         }
-        const int64_t n = tile_weight_row(d, tn, tid);
-        for (int g = 0; g < ng; ++g)  // the codes count units of 2^-9
-            t.swt[(tn * t.G + g0 + g) * 256 + tid] = 512.0f * d.sw[n * t.G + g0 + g];
+        if (tid < kUnit) {  // the codes count units of 2^-9
+            const int64_t n = unit_weight_row(d, u, tid);
+            for (int h = g0; h < min(g0 + 2, t.G); ++h)
+                t.swt[(u * t.G + h) * kUnit + tid] = 512.0f * d.sw[n * t.G + h];
+        }
+        uint8_t* dst = t.wq + (u * t.G + g0 + g) * kUnitCodes;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 32 * i + (tid >> 3);
+            const v8i c = int4_to_fp8(w[i]);
+            if (in) {
+                *(v4i*)(dst + 16 * slot(r, 2 * q)) = v4i{c[0], c[1], c[2], c[3]};
+                *(v4i*)(dst + 16 * slot(r, 2 * q + 1)) = v4i{c[4], c[5], c[6], c[7]};
+            }
+        }
         return;
     }
-    b -= t.tiles_n * pairs;
+    b -= (int64_t)t.units_n * pairs;
     const int64_t chunks = (t.G + 7) / 8;
-    const int64_t tm = b / chunks;
-    const int g0 = 8 * (int)(b - tm * chunks);
-    const int64_t m = min(tm * t.bm + min(tid, t.bm - 1), d.M - 1);
-    for (int g = g0; g < min(g0 + 8, t.G); ++g)
-        t.sat[(tm * t.G + g) * 256 + tid] = d.sa[m * t.G + g];
+    const int64_t u = b / chunks;
+    const int g0 = 8 * (int)(b - u * chunks);
+    const int64_t m = min(u * kUnit + (tid & 127), d.M - 1);
+    for (int g = g0 + (tid >> 7); g < min(g0 + 8, t.G); g += 2)
+        t.sat[(u * t.G + g) * kUnit + (tid & 127)] = d.sa[m * t.G + g];
 }
 
-template <int BM>
-__global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
+namespace {
+
+// scales of ROWS rows of one group: 256 as one 16-byte load per lane, 128 as
+// two 4-byte ones (each LDS side is linear in the lane)
+template <int ROWS>
+__device__ __forceinline__ void lds_scales(const v4i& r, uint32_t lds, uint32_t v16, int lane, uint32_t soff)
 {
-    constexpr int kAStage = BM * kGroup;
-    constexpr int kStage = kAStage + kWStage + 2 * kScaleStage;
-    constexpr int kSl = BM / 2 / 16;     // 16-row slices per wave
-    constexpr int kALoads = BM / 64;     // 1 KB loads per wave and stage
-    constexpr int kEpiStride = 68;  // floats; 64 columns and a pad against bank conflicts
-    constexpr int kEpiWave = 64 * kEpiStride * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kStage > 8 * kEpiWave ? 2 * kStage : 8 * kEpiWave];
+    if constexpr (ROWS == 256) {
+        lds_load16(r, lds, v16, soff);
+    } else {
+        static_assert(ROWS == 128, "one or two units");
+        lds_load4(r, lds, 4 * lane, soff);
+        lds_load4(r, lds + 256, 256 + 4 * lane, soff);
+    }
+}
+
+}  // namespace
+
+// WM x WN waves of 16 SL rows x 64 weight rows each.
+template <int WM, int WN, int SL>
+struct Tile {
+    static constexpr int kBM = WM * SL * 16, kBN = WN * 64;
+    static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int kA = 0, kW = kBM * kGroup, kSw = kW + kBN * kGroup, kSa = kSw + kBN * 4;
+    static constexpr int kStage = kSa + kBM * 4;
+    static constexpr int kEpiStride = 68;  // floats; 64 columns and a pad against bank conflicts
+    static constexpr int kEpiWave = 64 * kEpiStride * 4;
+    static constexpr int kLds = 2 * kStage > WM * WN * kEpiWave ? 2 * kStage : WM * WN * kEpiWave;
+    static_assert(kBM % kUnit == 0 && kBN % kUnit == 0 && SL % 4 == 0 && kLds <= 160 * 1024, "tile");
+};
+
+template <int WM, int WN, int SL>
+__global__ __launch_bounds__(64 * WM * WN, 2) void dense_tile_kernel(const TileArgs t, const int32_t tiles_m,
+                                                                     const int32_t tiles_n)
+{
+    using L = Tile<WM, WN, SL>;
+    constexpr int kWaves = WM * WN;
+    constexpr int kALoads = L::kBM / 8 / kWaves;  // 1 KB loads per wave and stage
+    constexpr int kWLoads = L::kBN / 8 / kWaves;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[L::kLds];
 
     const DenseArgs& d = t.d;
     const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / WN, wn = wave % WN;
     const int G = t.G;
 
     // tile of this workgroup: an eighth of the numbering per XCD
-    const int total = t.tiles_m * t.tiles_n;
+    const int total = tiles_m * tiles_n;
     const int chunk = (total + 7) / 8;
     const int id = (int)(blockIdx.x & 7) * chunk + (int)(blockIdx.x >> 3);
-    if (id >= total || (int)(blockIdx.x >> 3) >= chunk)
+    if (id >= total)
         return;
-    const int band = id / (8 * t.tiles_n);
-    const int bh = min(8, t.tiles_m - 8 * band);
-    const int in_band = id - band * 8 * t.tiles_n;
+    const int band = id / (8 * tiles_n);
+    const int bh = min(8, tiles_m - 8 * band);
+    const int in_band = id - band * 8 * tiles_n;
     const int tm = 8 * band + in_band % bh, tn = in_band / bh;
 
-    const int64_t m0 = (int64_t)tm * BM;
-    const int rows = (int)min((int64_t)BM, d.M - m0);
+    const int64_t m0 = (int64_t)tm * L::kBM;
+    const int rows = (int)min((int64_t)L::kBM, d.M - m0);
+    // the tile's operands; units past the end are not read (their loads
+    // return zero: the resource ends with the last unit)
+    const int un = min(L::kBN / kUnit, t.units_n - tn * (L::kBN / kUnit));
+    const int um = min(L::kBM / kUnit, t.units_m - tm * (L::kBM / kUnit));
     const v4i ra = sgpr_rsrc(d.a + m0 * d.K, (uint32_t)(rows * d.K));
-    const v4i rw = sgpr_rsrc(t.wq + (int64_t)tn * G * kWStage, (uint32_t)((int64_t)G * kWStage));
-    const v4i rsw = sgpr_rsrc(t.swt + (int64_t)tn * G * 256, (uint32_t)((int64_t)G * kScaleStage));
-    const v4i rsa = sgpr_rsrc(t.sat + (int64_t)tm * G * 256, (uint32_t)((int64_t)G * kScaleStage));
+    const v4i rw = sgpr_rsrc(t.wq + (int64_t)tn * (L::kBN / kUnit) * G * kUnitCodes, (uint32_t)((int64_t)un * G * kUnitCodes));
+    const v4i rsw = sgpr_rsrc(t.swt + (int64_t)tn * L::kBN * G, (uint32_t)((int64_t)un * G * kUnitScales));
+    const v4i rsa = sgpr_rsrc(t.sat + (int64_t)tm * L::kBM * G, (uint32_t)((int64_t)um * G * kUnitScales));
     uint32_t va[kALoads];
 #pragma unroll
     for (int j = 0; j < kALoads; ++j) {
@@ -139,25 +185,31 @@ __global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
         const int r = sl >> 3, c = (sl & 7) ^ (r & 7);
         va[j] = (uint32_t)(min(r, rows - 1) * d.K + 16 * c);
     }
+    uint32_t vw[kWLoads];
+#pragma unroll
+    for (int j = 0; j < kWLoads; ++j) {
+        const int piece = wave * kWLoads + j;  // of 16 per unit
+        vw[j] = (uint32_t)((piece >> 4) * G * kUnitCodes + (piece & 15) * 1024 + lane * 16);
+    }
+    const uint32_t vs = (uint32_t)((lane >> 5) * G * kUnitScales + (lane & 31) * 16);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)smem;
     auto issue = [&](int g, int st) {
-        const uint32_t base = lds0 + (uint32_t)(st * kStage);
+        const uint32_t base = lds0 + (uint32_t)(st * L::kStage);
 #pragma unroll
         for (int j = 0; j < kALoads; ++j)
             lds_load16(ra, base + (uint32_t)((wave * kALoads + j) * 1024), va[j], (uint32_t)g * kGroup);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            lds_load16(rw, base + (uint32_t)(kAStage + (wave * 4 + j) * 1024), (uint32_t)((wave * 4 + j) * 1024 + lane * 16),
-                       (uint32_t)g * kWStage);
+        for (int j = 0; j < kWLoads; ++j)
+            lds_load16(rw, base + (uint32_t)(L::kW + (wave * kWLoads + j) * 1024), vw[j], (uint32_t)g * kUnitCodes);
         if (wave == 0)
-            lds_load16(rsw, base + kAStage + kWStage, lane * 16, (uint32_t)g * kScaleStage);
-        if (wave == 4)
-            lds_load16(rsa, base + kAStage + kWStage + kScaleStage, lane * 16, (uint32_t)g * kScaleStage);
+            lds_scales<L::kBN>(rsw, base + L::kSw, vs, lane, (uint32_t)g * kUnitScales);
+        if (wave == kWaves - 1)
+            lds_scales<L::kBM>(rsa, base + L::kSa, vs, lane, (uint32_t)g * kUnitScales);
     };
 
-    float acc[kSl][4][4];
+    float acc[SL][4][4];
 #pragma unroll
-    for (int s = 0; s < kSl; ++s)
+    for (int s = 0; s < SL; ++s)
 #pragma unroll
         for (int f = 0; f < 4; ++f)
 #pragma unroll
@@ -166,10 +218,10 @@ __global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
 
     // LDS offsets of the lane's operands in a stage; slice s and fragment f lie
     // at constant distances (16 rows do not change the swizzle)
-    const uint32_t oa0 = 16 * slot(BM / 2 * wm + c16, q), oa1 = 16 * slot(BM / 2 * wm + c16, 4 + q);
-    const uint32_t ob0 = kAStage + 16 * slot(64 * wn + c16, q), ob1 = kAStage + 16 * slot(64 * wn + c16, 4 + q);
-    const uint32_t osw = kAStage + kWStage + 4 * (64 * wn + 4 * q);
-    const uint32_t osa = kAStage + kWStage + kScaleStage + 4 * (BM / 2 * wm + c16);
+    const uint32_t oa0 = 16 * slot(16 * SL * wm + c16, q), oa1 = 16 * slot(16 * SL * wm + c16, 4 + q);
+    const uint32_t ob0 = L::kW + 16 * slot(64 * wn + c16, q), ob1 = L::kW + 16 * slot(64 * wn + c16, 4 + q);
+    const uint32_t osw = L::kSw + 4 * (64 * wn + 4 * q);
+    const uint32_t osa = L::kSa + 4 * (16 * SL * wm + c16);
     constexpr int kFrag = 16 * kGroup;  // bytes of 16 rows
 
     issue(0, 0);
@@ -178,7 +230,7 @@ __global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
         barrier();  // stage g is whole, and nobody reads stage g - 1 any more
         if (g + 1 < G)
             issue(g + 1, (g + 1) & 1);
-        const uint8_t* st = smem + (g & 1) * kStage;
+        const uint8_t* st = smem + (g & 1) * L::kStage;
         const uint8_t *pa0 = st + oa0, *pa1 = st + oa1, *pb0 = st + ob0, *pb1 = st + ob1;
         const uint8_t *psw = st + osw, *psa = st + osa;
         auto read = [&](const uint8_t* p0, const uint8_t* p1, int i) {
@@ -206,10 +258,10 @@ __global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
             acc[s][f][3] = fmaf(sw[f].w, raw[f][3] * sa_raw, acc[s][f][3]);
         };
 #pragma unroll
-        for (int s = 0; s < kSl; ++s) {
+        for (int s = 0; s < SL; ++s) {
             v8i next = av;
             float sa_next = sa;
-            if (s + 1 < kSl) {
+            if (s + 1 < SL) {
                 next = read(pa0, pa1, s + 1);
                 sa_next = *(const float*)(psa + 64 * (s + 1));
             }
@@ -226,12 +278,12 @@ __global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
         }
 #pragma unroll
         for (int f = 0; f < 4; ++f)
-            promote(kSl - 1, f);
+            promote(SL - 1, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // the first slice's MFMAs
 #pragma unroll
-        for (int i = 0; i < 4 * (kSl - 1); ++i) {
+        for (int i = 0; i < 4 * (SL - 1); ++i) {
             if (i % 4 == 0)
                 __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);  // the next slice's reads
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // one MFMA
@@ -243,33 +295,33 @@ __global__ __launch_bounds__(512, 2) void dense_tile_kernel(const TileArgs t)
     // contiguous piece and the epilogue's code stands here once.
     barrier();  // the last stage has been read by everyone
     const bool glu = d.act == W4A8_ACT_SWIGLU;
-    float* const mine = (float*)(smem + wave * kEpiWave);
+    float* const mine = (float*)(smem + wave * L::kEpiWave);
     const int cols = glu ? 8 : 16;  // float4 columns of outputs per wave
     const int c4 = lane & (cols - 1);
-    const int64_t n0 = glu ? (int64_t)tn * (kBN / 2) + 32 * wn + 4 * c4 : (int64_t)tn * kBN + 64 * wn + 4 * c4;
+    const int64_t n0 = glu ? (int64_t)tn * (L::kBN / 2) + 32 * wn + 4 * c4 : (int64_t)tn * L::kBN + 64 * wn + 4 * c4;
 #pragma unroll
-    for (int p = 0; p < kSl / 4; ++p) {
+    for (int p = 0; p < SL / 4; ++p) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 const float* v = acc[4 * p + s][f];
-                *(float4*)(mine + (16 * s + c16) * kEpiStride + 16 * f + 4 * q) = make_float4(v[0], v[1], v[2], v[3]);
+                *(float4*)(mine + (16 * s + c16) * L::kEpiStride + 16 * f + 4 * q) = make_float4(v[0], v[1], v[2], v[3]);
             }
         __builtin_amdgcn_wave_barrier();  // one wave: LDS operations stay in order
-        const int first = BM / 2 * wm + 64 * p;
+        const int first = 16 * SL * wm + 64 * p;
 #pragma unroll 1
         for (int r = lane / cols; r < 64; r += 64 / cols) {
             if (first + r >= rows)
                 break;
-            const float4 y = *(const float4*)(mine + r * kEpiStride + 4 * c4);
+            const float4 y = *(const float4*)(mine + r * L::kEpiStride + 4 * c4);
             const float yv[4] = {y.x, y.y, y.z, y.w};
             float uv[4] = {0, 0, 0, 0};
             if (glu) {
-                const float4 u = *(const float4*)(mine + r * kEpiStride + 32 + 4 * c4);
+                const float4 u = *(const float4*)(mine + r * L::kEpiStride + 32 + 4 * c4);
                 uv[0] = u.x, uv[1] = u.y, uv[2] = u.z, uv[3] = u.w;
             }
-            epilogue4(d, m0 + first + r, n0, yv, uv);
+            epilogue4(d, m0 + first + r, n0, yv, uv, load_epilogue4(d, m0 + first + r, n0));
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -282,32 +334,69 @@ TileArgs plan_tiles(void* ws, const DenseArgs& d, size_t* bytes)
     TileArgs t = {};
     t.d = d;
     t.G = (int32_t)(d.K / kGroup);
-    t.bm = 256;
-    const int64_t per = d.act == W4A8_ACT_SWIGLU ? kBN / 2 : kBN;
-    t.tiles_m = (int32_t)api::ceil_div(d.M, t.bm);
-    t.tiles_n = (int32_t)api::ceil_div(d.N, per);
+    t.units_m = (int32_t)api::ceil_div(d.M, kUnit);
+    t.units_n = (int32_t)api::ceil_div(d.N, d.act == W4A8_ACT_SWIGLU ? kUnit / 2 : kUnit);
     api::Carve c(ws);
-    t.wq = c.take<uint8_t>((size_t)t.tiles_n * t.G * kWStage);
-    t.swt = c.take<float>((size_t)t.tiles_n * t.G * 256);
-    t.sat = c.take<float>((size_t)t.tiles_m * t.G * 256);
+    t.wq = c.take<uint8_t>((size_t)t.units_n * t.G * kUnitCodes);
+    t.swt = c.take<float>((size_t)t.units_n * t.G * kUnit);
+    t.sat = c.take<float>((size_t)t.units_m * t.G * kUnit);
     *bytes = c.used;
     return t;
 }
 
-template <int BM>
+template <int WM, int WN, int SL>
 hipError_t launch_tiles(const TileArgs& t, hipStream_t s)
 {
-    const int64_t total = (int64_t)t.tiles_m * t.tiles_n;
-    const dim3 grid((unsigned)((total + 7) / 8 * 8));
-    hipLaunchKernelGGL(dense_tile_kernel<BM>, grid, dim3(512), 0, s, t);
+    using L = Tile<WM, WN, SL>;
+    const int64_t tiles_m = api::ceil_div(t.units_m, L::kBM / kUnit), tiles_n = api::ceil_div(t.units_n, L::kBN / kUnit);
+    const dim3 grid((unsigned)((tiles_m * tiles_n + 7) / 8 * 8));
+    hipLaunchKernelGGL((dense_tile_kernel<WM, WN, SL>), grid, dim3(L::kThreads), 0, s, t, (int32_t)tiles_m,
+                       (int32_t)tiles_n);
     return hipGetLastError();
 }
 
 }  // namespace
 
+namespace {
+
+// Predicted times (us), fitted on MI355X over M 256 to 8000, K 128 to 7168, R
+// 1000 to 7168.
+//
+// A round of 256 x 256 tiles, one per CU, takes 16 + 0.0165 K; 128 x 128
+// tiles, two per CU, 10.5 + 0.0096 K (up to 256 of them, one per CU: 7 +
+// 0.0073 K).  4096 x 7168 x 4096: 138 us with the large ones, 163 with the
+// small; 2048 x 7168 x 4096: 128 and 79; 4000 x 512 x 4000: 26 and 28.
+struct TileCost {
+    double us;
+    bool large;
+};
+TileCost tile_cost(int64_t M, int64_t K, int64_t R)
+{
+    const double k = (double)K;
+    const double t3 = (double)(api::ceil_div(M, 256) * api::ceil_div(R, 256));
+    const double t1 = (double)(api::ceil_div(M, 128) * api::ceil_div(R, 128));
+    const double large = ceil(t3 / 256) * (16 + 0.0165 * k);
+    const double small = t1 <= 256 ? 7 + 0.0073 * k : fmax(1.0, t1 / 512) * (10.5 + 0.0096 * k);
+    return TileCost{large <= small ? large : small, large <= small};
+}
+int64_t weight_rows(int64_t N, int act)
+{
+    return act == W4A8_ACT_SWIGLU ? 2 * N : N;
+}
+
+}  // namespace
+
+// The tiles with their first pass (a launch, 5 us and 0.38 ps a weight)
+// against the few-rows kernel, whose workgroups of 32 rows x 64 weight rows
+// decode the weights again for every 32 rows (4.2 ns + 3.67 ps K each, over
+// all CUs).  Both sides measured: 768 x 7168 x 4096 73 us and 51, 1024 x 2048 x
+// 7168 41 and 46, 1500 x 2048 x 2048 29 and 20, 4096 x 128 x 4096 22 and 38.
 bool use_dense_tiles(int64_t M, int64_t K, int64_t N, int act)
 {
-    return M >= 512;
+    const int64_t R = weight_rows(N, act);
+    const double k = (double)K;
+    const double rows = 4 + (double)api::ceil_div(M, 32) * (double)api::ceil_div(R, 64) * (4.2e-3 + 3.67e-6 * k);
+    return tile_cost(M, K, R).us + 5 + 3.8e-7 * (double)R * k < rows;
 }
 
 size_t dense_tiles_workspace(int64_t M, int64_t K, int64_t N, int act)
@@ -323,10 +412,13 @@ hipError_t launch_dense_tiles(const DenseArgs& d, void* ws, hipStream_t s)
 {
     size_t bytes;
     const TileArgs t = plan_tiles(ws, d, &bytes);
-    const int64_t blocks = (int64_t)t.tiles_n * ((t.G + 1) / 2) + (int64_t)t.tiles_m * ((t.G + 7) / 8);
+    const int64_t blocks = (int64_t)t.units_n * ((t.G + 1) / 2) + (int64_t)t.units_m * ((t.G + 7) / 8);
     hipLaunchKernelGGL(dense_expand_kernel, dim3((unsigned)blocks), dim3(256), 0, s, t);
     const hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : launch_tiles<256>(t, s);
+    if (e != hipSuccess)
+        return e;
+    return tile_cost(d.M, d.K, weight_rows(d.N, d.act)).large ? launch_tiles<2, 4, 8>(t, s)
+                                                              : launch_tiles<2, 2, 4>(t, s);
 }
 
 }  // namespace w4a8

@@ -257,7 +257,9 @@ struct DenseArgs {
     int64_t ldr;
     uint16_t* out;
     int64_t ldo;
-    int vec4;  // four columns of a row are 8-byte aligned in out and residual, N % 4 == 0
+    // four (two) columns of a row are 8-byte (4-byte) aligned in out and
+    // residual, and N is a multiple of them
+    int vec4, vec2;
 };
 size_t dense_epilogue_workspace(int64_t M, int64_t K, int64_t N, int act);
 hipError_t launch_dense_epilogue(const DenseArgs& a, void* ws, hipStream_t s);
