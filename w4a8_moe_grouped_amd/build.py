@@ -3,7 +3,10 @@
     python -m w4a8_moe_grouped_amd.build
 
 Every .hip file under csrc/ is compiled to an object under _build/ (in
-parallel), then linked into w4a8_moe_grouped_amd/libw4a8.so.
+parallel), then linked into w4a8_moe_grouped_amd/libw4a8.so.  csrc/binding.cpp,
+the native half of the Python binding's short calls, becomes
+w4a8_moe_grouped_amd/_binding.so beside it (host code only, against torch's
+headers).
 """
 from __future__ import annotations
 
@@ -19,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libw4a8.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -43,11 +47,32 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    for path in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", lib_dir, "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for binding.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, BINDING)
+
+
 def build(jobs: int = 8, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(jobs, 16))) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, srcs))
+        binding.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

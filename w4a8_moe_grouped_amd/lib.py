@@ -8,7 +8,6 @@ exception is raised.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 from typing import Optional
@@ -460,58 +459,28 @@ def moe_align(topk_ids: torch.Tensor, expert_begin: int, num_local_experts: int,
 
 
 # ---- the operators around the expert forward -----------------------------------------
-#
-# Small batches wait for the host, so these calls keep it short: outputs come
-# from empty_strided, the stream and the device from torch's raw accessors
-# (a 4-token norm_residual took 18 us on the host with torch.cuda's own, a
-# moe_route 12).
 
-TYPE_FP32, TYPE_BF16, TYPE_FP16 = 0, 1, 2
-_TYPES = {torch.float32: TYPE_FP32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16}
-_ROW_TYPES = {torch.float32: TYPE_FP32, torch.bfloat16: TYPE_BF16}
 SCORES = {"sigmoid": 0, "softmax": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
 
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_empty = torch.empty_strided
+_native = None
 
 
-def _index(t: torch.Tensor) -> int:
-    i = t.get_device()
-    if i < 0:
-        raise W4A8Error("all tensors must be on the GPU")
-    return i
-
-
-def _addr(t: Optional[torch.Tensor], index: int):
-    if t is None:
-        return None
-    if t.get_device() != index:
-        raise W4A8Error("all tensors must be on one GPU")
-    return t.data_ptr()
-
-
-def _type(t: torch.Tensor, types: dict) -> int:
-    kind = types.get(t.dtype)
-    if kind is None:
-        raise W4A8Error("unsupported tensor type %s" % t.dtype)
-    return kind
-
-
-def _rows(t: torch.Tensor, rows: int, cols: int, what: str) -> int:
-    """Row stride of a [rows, cols] tensor with unit column stride."""
-    if t.shape != (rows, cols):
-        raise W4A8Error("%s must be [%d, %d], not %s" % (what, rows, cols, list(t.shape)))
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1:
-        raise W4A8Error("%s must have unit column stride" % what)
-    return ld if rows > 1 else cols
-
-
-def _whole(t: torch.Tensor, shape: tuple, dtype: torch.dtype, what: str):
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        raise W4A8Error("%s must be a contiguous %s tensor of shape %s" % (what, dtype, list(shape)))
+def _binding():
+    """The native half of the calls below (csrc/binding.cpp), built beside
+    libw4a8.so."""
+    global _native
+    if _native is None:
+        L = load()
+        try:
+            from w4a8_moe_grouped_amd import _binding as native
+        except ImportError as e:
+            raise W4A8Error("_binding.so not built (run python -m w4a8_moe_grouped_amd.build): %s" % e)
+        native.init(W4A8Error, torch._C._cuda_getCurrentRawStream,
+                    *[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                        L.w4a8_status_string, L.w4a8_moe_route, L.w4a8_norm_residual, L.w4a8_gemm_epilogue)])
+        _native = native
+    return _native
 
 
 def moe_route(logits: torch.Tensor, topk: int, score: str = "sigmoid", bias: Optional[torch.Tensor] = None,
@@ -522,35 +491,11 @@ def moe_route(logits: torch.Tensor, topk: int, score: str = "sigmoid", bias: Opt
     int32 [T, topk], topk_weights fp32 [T, topk]) as the fused forward reads
     them.  bias: fp32 [E], added to the scores that choose; num_tokens: a
     one-element int32 device tensor, rows from it on get id -1 and weight 0."""
-    index = _index(logits)
-    if index != _current_device():
-        with torch.cuda.device(index):
-            return moe_route(logits, topk, score, bias, num_groups, topk_groups, group_top, renormalize,
-                             scale, num_tokens, topk_ids, topk_weights)
-    if logits.dim() != 2 or score not in SCORES:
-        raise W4A8Error("logits must be [T, E] and score one of %s" % (tuple(SCORES),))
-    T, E = logits.shape
-    if not 0 < topk <= E:
-        raise W4A8Error("topk must be in 1..E")
-    if bias is not None:
-        _whole(bias, (E,), torch.float32, "bias")
-    if num_tokens is not None and (num_tokens.numel() != 1 or num_tokens.dtype != torch.int32):
-        raise W4A8Error("num_tokens must be one int32")
-    if topk_ids is None:
-        topk_ids = _empty((T, topk), (topk, 1), dtype=torch.int32, device=logits.device)
-    else:
-        _whole(topk_ids, (T, topk), torch.int32, "topk_ids")
-    if topk_weights is None:
-        topk_weights = _empty((T, topk), (topk, 1), dtype=torch.float32, device=logits.device)
-    else:
-        _whole(topk_weights, (T, topk), torch.float32, "topk_weights")
-    rc = load().w4a8_moe_route(
-        logits.data_ptr(), _type(logits, _TYPES), T, E, _rows(logits, T, E, "logits"), _addr(bias, index),
-        SCORES[score], num_groups, topk_groups, group_top, topk, 1 if renormalize else 0, scale,
-        _addr(num_tokens, index), _addr(topk_ids, index), _addr(topk_weights, index), _raw_stream(index))
-    if rc:
-        _check(rc, "w4a8_moe_route")
-    return topk_ids, topk_weights
+    kind = SCORES.get(score)
+    if kind is None:
+        raise W4A8Error("score must be one of %s" % (tuple(SCORES),))
+    return (_native or _binding()).moe_route(logits, topk, kind, bias, num_groups, topk_groups, group_top,
+                                             renormalize, scale, num_tokens, topk_ids, topk_weights)
 
 
 def norm_residual(x: Optional[torch.Tensor], residual: Optional[torch.Tensor],
@@ -568,87 +513,11 @@ def norm_residual(x: Optional[torch.Tensor], residual: Optional[torch.Tensor],
     None without pre_weight.  keep_residual=False: r' is not written.
     residual_out, out and out_scales may be given; residual_out may be
     residual itself."""
-    like = residual if residual is not None else x
-    if like is None:
-        raise W4A8Error("x or residual must be given")
-    index = _index(like)
-    if index != _current_device():
-        with torch.cuda.device(index):
-            return norm_residual(x, residual, post_weight, gate, residual_scale, pre_weight, weight_offset,
-                                 eps, quantize, keep_residual, residual_out, out, out_scales)
-    if like.dim() != 2:
-        raise W4A8Error("x and residual must be [T, H]")
-    T, H = like.shape
-    device = like.device
-    r_type = x_type = _type(like, _ROW_TYPES)
-    ldx = ldr = ldr_out = ldy = H
-    if residual is not None:
-        ldr = _rows(residual, T, H, "residual")
-    if x is not None:
-        ldx, x_type = _rows(x, T, H, "x"), _type(x, _ROW_TYPES)
-    p_type = None
-    for w in (post_weight, pre_weight, gate):
-        if w is not None:
-            kind = _type(w, _ROW_TYPES)
-            if p_type is not None and kind != p_type:
-                raise W4A8Error("post_weight, pre_weight and gate must be of one type")
-            p_type = kind
-            if w is not gate and (w.shape != (H,) or not w.is_contiguous()):
-                raise W4A8Error("a norm's weight must be a contiguous [H]")
-    gate_rs = gate_cs = 0
-    if gate is not None:
-        if gate.shape == (H,) and gate.is_contiguous():
-            gate_cs = 1
-        elif gate.shape == (T, H):
-            gate_rs, gate_cs = _rows(gate, T, H, "gate"), 1
-        elif gate.shape == (T, 1):
-            gate_rs = gate.stride(0) if T > 1 else 1
-        else:
-            raise W4A8Error("gate must be a contiguous [H], or [T, H] or [T, 1]")
-    if residual_out is not None:
-        if residual_out.dtype != like.dtype or not keep_residual:
-            raise W4A8Error("residual_out must have the residual's type")
-        ldr_out = _rows(residual_out, T, H, "residual_out")
-    elif keep_residual:
-        residual_out = _empty((T, H), (H, 1), dtype=like.dtype, device=device)
-    y = codes = None
-    if pre_weight is None:
-        if quantize or out is not None or out_scales is not None:
-            raise W4A8Error("an output y needs pre_weight")
-    elif quantize:
-        if H % GROUP != 0:
-            raise W4A8Error("quantize needs H %% %d == 0" % GROUP)
-        G = H // GROUP
-        if out is None:
-            out = _empty((T, H), (H, 1), dtype=torch.uint8, device=device)
-        else:
-            _whole(out, (T, H), torch.uint8, "out")
-        if out_scales is None:
-            out_scales = _empty((T, G), (G, 1), dtype=torch.float32, device=device)
-        else:
-            _whole(out_scales, (T, G), torch.float32, "out_scales")
-        codes = _addr(out, index)
-    else:
-        if out is None:
-            out = _empty((T, H), (H, 1), dtype=torch.bfloat16, device=device)
-        else:
-            if out.dtype != torch.bfloat16:
-                raise W4A8Error("out must be bf16")
-            ldy = _rows(out, T, H, "out")
-        if out_scales is not None:
-            raise W4A8Error("out_scales needs quantize")
-        y = _addr(out, index)
-    rc = load().w4a8_norm_residual(
-        _addr(x, index), x_type, ldx, _addr(residual, index), r_type, ldr, T, H, p_type or 0,
-        _addr(post_weight, index), _addr(gate, index), gate_rs, gate_cs, residual_scale,
-        _addr(pre_weight, index), weight_offset, eps, _addr(residual_out, index), ldr_out, y, ldy, codes,
-        _addr(out_scales, index), _raw_stream(index))
-    if rc:
-        _check(rc, "w4a8_norm_residual")
-    return residual_out, out, out_scales
+    return (_native or _binding()).norm_residual(x, residual, post_weight, gate, residual_scale, pre_weight,
+                                                 weight_offset, eps, quantize, keep_residual, residual_out,
+                                                 out, out_scales)
 
 
-@functools.lru_cache(maxsize=1024)
 def gemm_epilogue_workspace_bytes(M: int, K: int, N: int, activation: str = "none") -> int:
     n = ctypes.c_size_t(0)
     _check(load().w4a8_gemm_epilogue(None, None, M, K, None, None, N, None, 0, ACTIVATIONS[activation], None,
@@ -664,56 +533,10 @@ def gemm_epilogue(a_q: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
     a_scales, w, w_scales as for gemm; with activation "swiglu" w has 2N rows
     (gate rows, then up rows).  bias: fp32 or bf16, one value per weight row;
     residual: bf16 [M, N], may be out itself."""
-    index = _index(a_q)
-    if index != _current_device():
-        with torch.cuda.device(index):
-            return gemm_epilogue(a_q, a_scales, w, w_scales, bias, activation, residual, out, workspace)
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise W4A8Error("activation must be one of %s" % (tuple(ACTIVATIONS),))
-    if a_q.dim() != 2 or w.dim() != 2:
-        raise W4A8Error("a_q must be [M, K] and w [rows, K/2]")
-    M, K = a_q.shape
-    R = N = w.shape[0]
-    if activation == "swiglu":
-        N = R // 2
-    G = K // GROUP
-    if w.shape[1] * 2 != K or N == 0 or (R != N and R != 2 * N):
-        raise W4A8Error("bad operand shapes")
-    _whole(a_q, (M, K), torch.uint8, "a_q")
-    _whole(a_scales, (M, G), torch.float32, "a_scales")
-    _whole(w, (R, K // 2), torch.uint8, "w")
-    _whole(w_scales, (R, G), torch.float32, "w_scales")
-    bias_type = 0
-    if bias is not None:
-        bias_type = _type(bias, _ROW_TYPES)
-        _whole(bias, (R,), bias.dtype, "bias")
-    ldr = ldo = N
-    if residual is not None:
-        if residual.dtype != torch.bfloat16:
-            raise W4A8Error("residual must be bf16")
-        ldr = _rows(residual, M, N, "residual")
-    if out is None:
-        out = _empty((M, N), (N, 1), dtype=torch.bfloat16, device=a_q.device)
-    else:
-        if out.dtype != torch.bfloat16:
-            raise W4A8Error("out must be bf16")
-        ldo = _rows(out, M, N, "out")
-    if M == 0:
-        return out
-    need = gemm_epilogue_workspace_bytes(M, K, N, activation)
-    if workspace is None:
-        # a call that needs none still names a buffer (NULL asks for the size)
-        workspace = torch.empty(need, dtype=torch.uint8, device=a_q.device) if need else out
-    else:
-        need = workspace.numel() * workspace.element_size()
-    rc = load().w4a8_gemm_epilogue(
-        a_q.data_ptr(), _addr(a_scales, index), M, K, _addr(w, index), _addr(w_scales, index), N,
-        _addr(bias, index), bias_type, act, _addr(residual, index), ldr, _addr(out, index), ldo,
-        _addr(workspace, index), ctypes.byref(ctypes.c_size_t(need)), _raw_stream(index))
-    if rc:
-        _check(rc, "w4a8_gemm_epilogue")
-    return out
+    return (_native or _binding()).gemm_epilogue(a_q, a_scales, w, w_scales, bias, act, residual, out, workspace)
 
 
 STAGES = ("align", "quant", "gate_up", "down", "combine")
