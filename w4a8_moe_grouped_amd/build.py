@@ -59,7 +59,8 @@ def _build_binding() -> None:
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
     for path in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
         cmd += ["-isystem", path]
-    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", lib_dir, "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", lib_dir, "-lc10", "-ltorch_cpu", "-ltorch_hip",
+            "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for binding.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr))

@@ -10,7 +10,7 @@
 
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 
 #include <stdexcept>
@@ -136,9 +136,10 @@ void whole(const at::Tensor& t, at::IntArrayRef shape, at::ScalarType type, cons
         refuse(std::string(what) + " must be a contiguous " + c10::toString(type) + " tensor of shape " + name(shape));
 }
 
+// an output: torch's caching allocator, without the way through its dispatcher
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Device& device)
 {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    return at::Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
 void need_gpu(const at::Tensor& t)
