@@ -181,8 +181,27 @@ __global__ __launch_bounds__(64 * WAVES) void dense_rows_kernel(const DenseArgs 
         for (int i = 0; i < D; ++i)
             if (i < n)
                 issue(c0 + i, i);
-        int st = 0;
-        for (int i = 0; i < n; ++i) {
+        int st = 0, i = 0;
+        if constexpr (D % 2 == 0 && D > 2) {
+            // two groups at a time: one's matrix products run under the other's
+            // decode (1 x 7168 x 4096: 7.4 us against 7.9)
+            for (; i + 1 < n; i += 2) {
+                if (n - 2 - i >= D - 2)
+                    wait_vmcnt<(D - 2) * kLoads>();
+                else
+                    wait_vmcnt<0>();
+                asm volatile("" ::: "memory");
+                multiply(mine + st * Lds::kStage, i);
+                multiply(mine + (st + 1) * Lds::kStage, i + 1);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (i + D + j < n)
+                        issue(c0 + i + D + j, st + j);
+                st = st + 2 == D ? 0 : st + 2;
+            }
+        }
+        for (; i < n; ++i) {
             // group i (and the scales before it) landed; up to D - 1 behind it fly
             if (D > 1 && n - 1 - i >= D - 1)
                 wait_vmcnt<(D - 1) * kLoads>();
