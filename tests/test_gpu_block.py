@@ -419,6 +419,19 @@ def test_gemm_epilogue_strides_and_in_place(dev, M, N, extra):
     check_gemm(ops, residual=res, got=w4.gemm_epilogue(*ops, residual=rr, out=rr))
 
 
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh", "swiglu"])
+def test_gemm_epilogue_activation_of_every_size(dev, act):
+    """The activation alone, on biases from -60 to 60 and near 0 (zero codes)."""
+    v = torch.cat([torch.linspace(-60, 60, 4001, device=dev), torch.logspace(-30, 0, 200, device=dev),
+                   -torch.logspace(-30, 0, 200, device=dev), torch.zeros(3, device=dev)])
+    bias = torch.cat([v, torch.ones_like(v)]) if act == "swiglu" else v
+    q, s, w, sw = gemm_inputs(dev, 2, 128, bias.numel())
+    check_gemm((torch.zeros_like(q), s, w, sw), activation=act, bias=bias)
+    bias[0], bias[1] = INF, math.nan
+    out = w4.gemm_epilogue(torch.zeros_like(q), s, w, sw, activation=act, bias=bias)
+    assert bool((out[:, 0] == INF).all()) and bool(torch.isnan(out[:, 1]).all())
+
+
 def test_gemm_epilogue_special_values(dev):
     """Scales of inf and NaN reach their own outputs and no others."""
     q, s, w, sw = gemm_inputs(dev, 40, 512, 64)
