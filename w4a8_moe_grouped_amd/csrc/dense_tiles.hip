@@ -63,51 +63,48 @@ __device__ __forceinline__ int64_t unit_weight_row(const DenseArgs& d, int64_t u
 
 }  // namespace
 
-// Blocks [0, units_n * ceil(G/2)): two groups (a row's 128 bytes) of one unit
-// of weights; then units_m * ceil(G/8) blocks: eight groups of activation
-// scales of one unit of rows.
+// Blocks [0, 4 * units_n * ceil(G/2)): two groups (a row's 128 bytes) of a
+// quarter of one unit of weights; then units_n * ceil(G/8) blocks: eight
+// groups of weight scales of one unit; then units_m * ceil(G/8): of activation
+// scales.  Short blocks: a pass this small is bound by latency.
 __global__ __launch_bounds__(256) void dense_expand_kernel(const TileArgs t)
 {
     const DenseArgs& d = t.d;
     const int tid = threadIdx.x;
-    const int pairs = (t.G + 1) / 2;
-    int64_t b = blockIdx.x;
-    if (b < (int64_t)t.units_n * pairs) {
-        const int64_t u = (int)blockIdx.x / pairs;
-        const int g0 = 2 * ((int)blockIdx.x - (int)u * pairs);
-        // 16 packed bytes an item: eight of one row lie in one 128-byte line
-        const int g = (tid >> 2) & 1, q = tid & 3;
-        const bool in = g0 + g < t.G;
-        v4i w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t n = unit_weight_row(d, u, 32 * i + (tid >> 3));
-            w[i] = ldg16_nt(d.w + n * (d.K / 2) + (int64_t)(in ? g0 + g : g0) * (kGroup / 2) + 16 * q);
-        }
-        if (tid < kUnit) {  // the codes count units of 2^-9
-            const int64_t n = unit_weight_row(d, u, tid);
-            for (int h = g0; h < min(g0 + 2, t.G); ++h)
-                t.swt[(u * t.G + h) * kUnit + tid] = 512.0f * d.sw[n * t.G + h];
-        }
-        uint8_t* dst = t.wq + (u * t.G + g0 + g) * kUnitCodes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 32 * i + (tid >> 3);
-            const v8i c = int4_to_fp8(w[i]);
-            if (in) {
-                *(v4i*)(dst + 16 * slot(r, 2 * q)) = v4i{c[0], c[1], c[2], c[3]};
-                *(v4i*)(dst + 16 * slot(r, 2 * q + 1)) = v4i{c[4], c[5], c[6], c[7]};
-            }
-        }
+    const int pairs = (t.G + 1) / 2, eights = (t.G + 7) / 8;
+    int b = (int)blockIdx.x;
+    if (b < 4 * t.units_n * pairs) {
+        // 16 packed bytes a thread: eight of one row lie in one 128-byte line
+        const int r = 32 * (b & 3) + (tid >> 3), g = (tid >> 2) & 1, q = tid & 3;
+        const int64_t u = (b >> 2) / pairs;
+        const int group = 2 * ((b >> 2) - (int)u * pairs) + g;
+        if (group >= t.G)
+            return;
+        const int64_t n = unit_weight_row(d, u, r);
+        const v8i c = int4_to_fp8(ldg16_nt(d.w + n * (d.K / 2) + (int64_t)group * (kGroup / 2) + 16 * q));
+        uint8_t* dst = t.wq + (u * t.G + group) * kUnitCodes;
+        *(v4i*)(dst + 16 * slot(r, 2 * q)) = v4i{c[0], c[1], c[2], c[3]};
+        *(v4i*)(dst + 16 * slot(r, 2 * q + 1)) = v4i{c[4], c[5], c[6], c[7]};
         return;
     }
-    b -= (int64_t)t.units_n * pairs;
-    const int64_t chunks = (t.G + 7) / 8;
-    const int64_t u = b / chunks;
-    const int g0 = 8 * (int)(b - u * chunks);
-    const int64_t m = min(u * kUnit + (tid & 127), d.M - 1);
-    for (int g = g0 + (tid >> 7); g < min(g0 + 8, t.G); g += 2)
-        t.sat[(u * t.G + g) * kUnit + (tid & 127)] = d.sa[m * t.G + g];
+    b -= 4 * t.units_n * pairs;
+    const bool weights = b < t.units_n * eights;
+    if (!weights)
+        b -= t.units_n * eights;
+    const int64_t u = b / eights;
+    const int g0 = 8 * (b - (int)u * eights) + 4 * (tid >> 7), r = tid & (kUnit - 1);
+    const int64_t row = weights ? unit_weight_row(d, u, r) : min(u * kUnit + r, d.M - 1);
+    const float* src = (weights ? d.sw : d.sa) + row * t.G;
+    float* dst = (weights ? t.swt : t.sat) + u * t.G * kUnit + r;
+    const float mul = weights ? 512.0f : 1.0f;  // the codes count units of 2^-9
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = g0 + i < t.G ? src[g0 + i] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (g0 + i < t.G)
+            dst[(int64_t)(g0 + i) * kUnit] = mul * v[i];
 }
 
 namespace {
@@ -412,7 +409,9 @@ hipError_t launch_dense_tiles(const DenseArgs& d, void* ws, hipStream_t s)
 {
     size_t bytes;
     const TileArgs t = plan_tiles(ws, d, &bytes);
-    const int64_t blocks = (int64_t)t.units_n * ((t.G + 1) / 2) + (int64_t)t.units_m * ((t.G + 7) / 8);
+    const int64_t blocks = 4 * (int64_t)t.units_n * ((t.G + 1) / 2) + (int64_t)(t.units_n + t.units_m) * ((t.G + 7) / 8);
+    if (blocks > INT32_MAX)
+        return hipErrorInvalidValue;
     hipLaunchKernelGGL(dense_expand_kernel, dim3((unsigned)blocks), dim3(256), 0, s, t);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
