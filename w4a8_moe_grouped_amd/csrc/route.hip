@@ -510,20 +510,19 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N])
                     }
 }
 
-// other groups of the row, one rotation after another: how many are better
-// than this lane's, and whether any is too close to tell
+// other groups of the row, one rotation after another (lane l reads l - N, a
+// lower group unless that wraps): how many are better than this lane's, and
+// whether any is too close to tell
 template <int N>
-__device__ __forceinline__ void rank_groups(float mine, int group, int run, float slack, int& better, bool& close)
+__device__ __forceinline__ void rank_groups(float mine, int l, int run, float slack, int& better, bool& close)
 {
     if constexpr (N < 16) {
         if ((N & (run - 1)) == 0) {
             const float v = dpp_f<kRor + N>(mine);
-            const int g = (int)dpp_u<kRor + N>((uint32_t)group);
-            better += (v > mine || (v == mine && g < group)) ? 1 : 0;
-            // two equal infinities (false here) tie in 64 bits too
-            close |= fabsf(v - mine) <= slack + dpp_f<kRor + N>(slack);
+            better += (v > mine || (v == mine && l >= N)) ? 1 : 0;
+            close |= fabsf(v - mine) <= slack;  // two equal infinities (false here) tie in 64 bits too
         }
-        rank_groups<N + 1>(mine, group, run, slack, better, close);
+        rank_groups<N + 1>(mine, l, run, slack, better, close);
     }
 }
 
@@ -668,10 +667,13 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
         // logits compare exactly; a sum is off by as much as both its terms,
         // whose magnitudes count where they cancel
         float slack = -1.0f;
-        if (KEY == KEY_CHOICE || sums)
-            slack = 2.0f * off + 0x1p-22f * (fabsf(v1) + (two ? fabsf(v2) : 0.0f));
+        if (KEY == KEY_CHOICE || sums) {
+            slack = 4.0f * off + 0x1p-21f * (fabsf(v1) + (two ? fabsf(v2) : 0.0f));
+            // of any two groups of the row (infinite where one is: all close)
+            slack = __uint_as_float(row_max(v1 > ninf ? __float_as_uint(slack) : 0));
+        }
         int better = 0;
-        rank_groups<1>(two ? v1 + v2 : v1, l / run, run, slack, better, close);
+        rank_groups<1>(two ? v1 + v2 : v1, l, run, slack, better, close);
         open = better < a.kept;
     }
 #pragma unroll
