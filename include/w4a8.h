@@ -501,8 +501,9 @@ int w4a8_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, in
  *   y_bf16       [T, H] bf16, row stride ldy, or NULL
  *   q_e4m3       [T, H] e4m3 codes of y, row stride H, with
  *   q_scales     [T, H/128] fp32, by the rule of w4a8_quantize_act on the
- *                unrounded y; both or neither
- * T >= 0 (T == 0 launches nothing), H > 0, eps > 0; pre_weight and an output
+ *                unrounded y (a block with a NaN has the scale NaN); both or
+ *                neither
+ * T >= 0 (T == 0 launches nothing), H > 0, eps >= 2^-126; pre_weight and an output
  * of y go together, and so do a missing pre_weight and none; x or residual
  * must be given, and some output; post_weight and gate need x (INVALID_ARG
  * otherwise).  H <= 32768, T < 2^31, H % 128 == 0 with codes, pointers

@@ -51,7 +51,7 @@ def _norm(L, x=P, xt=1, ldx=256, r=P2, rt=1, ldr=256, T=0, H=256, pt=1, post=Non
 
 
 @pytest.mark.parametrize("change, want", [
-    (dict(), OK), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(eps=0.0), INVALID), (dict(eps=math.nan), INVALID),
+    (dict(), OK), (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(eps=0.0), INVALID), (dict(eps=math.nan), INVALID), (dict(eps=1e-40), INVALID),
     (dict(xt=2), INVALID), (dict(rt=3), INVALID), (dict(pt=2), INVALID), (dict(q=P), INVALID), (dict(qs=P), INVALID),
     (dict(ldx=255), INVALID), (dict(ldr=255), INVALID), (dict(ldo=255), INVALID), (dict(ldy=255), INVALID),
     (dict(gate=P, gcs=2), INVALID), (dict(gate=P, gcs=1, grs=255), INVALID), (dict(gate=P, grs=-1), INVALID),

@@ -283,6 +283,9 @@ def test_norm_special_rows(dev):
     out, y, _ = w4.norm_residual(x, r, post_weight=w, pre_weight=w)
     assert bool(torch.isfinite(out[[0, 1, 2, 5]]).all()) and bool(torch.isfinite(y[[0, 1, 2, 5]]).all())
     assert bool(torch.isnan(y[[3, 4]]).any(-1).all())
+    # codes hold no NaN that the clamp leaves: the block's scale is NaN
+    _, q, scale = w4.norm_residual(x, r, post_weight=w, pre_weight=w, quantize=True)
+    assert torch.isnan(scale).any(-1).tolist() == [False, False, False, True, True, False]
     # a NaN stays one in bf16 too
     _, y, _ = w4.norm_residual(None, x, pre_weight=w.to(BF16))
     assert bool(torch.isnan(y[4]).all())
@@ -587,6 +590,59 @@ def test_block_on_another_stream(dev):
     for name, v in want.items():
         if name != "logits":
             assert torch.equal(again[name], v), name
+
+
+def test_gemm_epilogue_tiles_in_a_graph(dev):
+    """The two launches of the tiles, captured and replayed on new operands,
+    with eager calls and synchronisations in between."""
+    M, K, N = 4096, 256, 4096
+    ops = [t.clone() for t in gemm_inputs(dev, M, K, N)]
+    assert w4.gemm_epilogue_workspace_bytes(M, K, N) > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        w4.gemm_epilogue(*ops)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = w4.gemm_epilogue(*ops, activation="silu")
+    for k in range(4):
+        new = gemm_inputs(dev, M, K, N, seed=k)
+        for t, u in zip(ops, new):
+            t.copy_(u)
+        graph.replay()
+        want = w4.gemm_epilogue(*new, activation="silu")
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), k
+    del graph
+
+
+@pytest.mark.parametrize("M, K, N", [(64, 2048, 512), (4096, 256, 4096)])
+def test_two_streams_at_once(dev, M, K, N):
+    """Calls that overlap on two streams, each with its own outputs."""
+    sets = [gemm_inputs(dev, M, K, N, seed=k) for k in range(2)]
+    rows = [norm_inputs(dev, M, 1024, BF16, FP32, FP32, seed=k) for k in range(2)]
+    logits = [torch.randn(M, 256, device=dev, generator=gen(dev, k)) for k in range(2)]
+
+    def calls(k):
+        d = rows[k]
+        return (w4.gemm_epilogue(*sets[k], activation="gelu"),
+                *w4.norm_residual(d["x"], d["residual"], post_weight=d["post"], pre_weight=d["pre"], quantize=True),
+                *w4.moe_route(logits[k], 8, num_groups=8, topk_groups=4))
+
+    want = [calls(k) for k in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(calls(k))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for one in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(one, want[k]))
 
 
 def test_binding_checks_on_the_gpu(dev):

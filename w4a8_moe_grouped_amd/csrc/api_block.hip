@@ -7,7 +7,7 @@
 #include "api_util.hpp"
 #include "internal.hpp"
 
-#include <math.h>
+#include <float.h>
 
 namespace {
 
@@ -80,7 +80,7 @@ int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* resid
                        void* y_bf16, int64_t ldy, uint8_t* q_e4m3, float* q_scales,
                        hipStream_t stream)
 {
-    if (T < 0 || H <= 0 || !(eps > 0.0f) || !float_or_bf16(x_type) || !float_or_bf16(residual_type) ||
+    if (T < 0 || H <= 0 || !(eps >= FLT_MIN) || !float_or_bf16(x_type) || !float_or_bf16(residual_type) ||
         !float_or_bf16(param_type))
         return W4A8_ERR_INVALID_ARG;
     const bool want_y = y_bf16 != nullptr || q_e4m3 != nullptr;

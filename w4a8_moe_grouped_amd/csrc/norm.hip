@@ -93,6 +93,15 @@ __device__ __forceinline__ void store8(uint16_t* p, int h, int H, const float* v
             p[h + i] = (uint16_t)(d[i / 2] >> (16 * (i & 1)));
 }
 
+// the maximum of 16 neighbouring lanes
+__device__ __forceinline__ uint32_t block_max(uint32_t v)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
+    return v;
+}
+
 // the row's sum; s_part: one float per wave of the workgroup
 template <bool WAVE_ROW>
 __device__ __forceinline__ float row_sum(float v, float* s_part)
@@ -206,11 +215,14 @@ __global__ __launch_bounds__(WAVE_ROW ? 64 * kNRows : 1024) void norm_kernel(con
         if (a.q != nullptr) {
             // H is a multiple of 128: the 16 lanes of a block are all inside
             // the row or all behind it
-            float amax = 0.0f;
+            // magnitudes as integers: a NaN is the largest, and makes the
+            // block's scale NaN
+            uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                amax = fmaxf(amax, fabsf(v[c][i]));
-            amax = clamp_amax(group_max<16>(amax));
+                top = max(top, __float_as_uint(v[c][i]) & 0x7FFFFFFFu);
+            top = block_max(top);
+            const float amax = clamp_amax(__uint_as_float(top));
             const float inv = recip448(amax);
             uint32_t d[4];
 #pragma unroll
@@ -219,7 +231,8 @@ __global__ __launch_bounds__(WAVE_ROW ? 64 * kNRows : 1024) void norm_kernel(con
             if (h < H) {
                 *(uint2*)(a.q + t * H + h) = make_uint2(d[0] | (d[1] << 16), d[2] | (d[3] << 16));
                 if ((tid & 15) == 0)
-                    a.q_scales[t * (H / kGroup) + h / kGroup] = scale_of(amax);
+                    a.q_scales[t * (H / kGroup) + h / kGroup] =
+                        top > 0x7F800000u ? __uint_as_float(top) : scale_of(amax);
             }
         }
     }
