@@ -59,7 +59,8 @@ def check_route(logits, topk, got=None, **kw):
 @pytest.mark.parametrize("T, E, k, groups, kept", [
     (1, 8, 2, 1, 1), (64, 256, 8, 8, 4), (5, 256, 8, 1, 1), (33, 90, 6, 6, 3), (7, 1, 1, 1, 1), (9, 64, 32, 2, 2),
     (3, 1000, 10, 8, 2), (2, 1024, 32, 64, 64), (17, 384, 8, 1, 1), (6, 130, 5, 13, 4), (130, 60, 4, 1, 1),
-    (4, 64, 3, 64, 5), (11, 160, 6, 8, 3), (3, 512, 7, 4, 1)])
+    (4, 64, 3, 64, 5), (11, 160, 6, 8, 3), (3, 512, 7, 4, 1), (9, 256, 16, 8, 4), (10, 100, 13, 1, 1), (6, 48, 16, 16, 9),
+    (7, 234, 9, 13, 5), (5, 256, 15, 16, 16), (8, 75, 10, 5, 2), (6, 128, 16, 2, 1), (5, 33, 12, 3, 3)])
 def test_route(dev, dtype, score, T, E, k, groups, kept):
     g = gen(dev, T * E + k)
     x = torch.randn(T, E, generator=g, device=dev).to(dtype)
@@ -108,7 +109,7 @@ def test_route_masked_and_special_values(dev, score, groups, kept):
 
 @pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
 @pytest.mark.parametrize("E, groups, kept", [(256, 8, 4), (256, 16, 5), (256, 2, 1), (192, 6, 2), (64, 8, 3), (128, 4, 2),
-                                             (100, 1, 1), (250, 1, 1)])
+                                             (100, 1, 1), (250, 1, 1), (90, 6, 3), (77, 7, 3), (165, 11, 4)])
 def test_route_near_ties(dev, dtype, E, groups, kept):
     """Logits a few steps of their type apart, and sums of choices whose parts
     cancel: the order is that of 64 bits."""
@@ -120,6 +121,7 @@ def test_route_near_ties(dev, dtype, E, groups, kept):
     for score in ("sigmoid", "softmax"):
         for bias in (None, torch.zeros(E, device=dev), wide, 1e-7 * torch.randn(E, generator=g, device=dev)):
             for top in (1, 2):
+                check_route(x[::3], 14, score=score, bias=bias, num_groups=groups, topk_groups=kept, group_top=top)
                 check_route(x, 8, score=score, bias=bias, num_groups=groups, topk_groups=kept, group_top=top)
 
 

@@ -210,7 +210,10 @@ struct RouteArgs {
     const float* bias;  // [E] or null
     int softmax;        // score: softmax, else sigmoid
     int32_t groups, kept, group_top;
-    int wide;           // set by the launcher: rows allow wide loads
+    // set by the launcher: rows allow wide loads; with 16 lanes per token, lanes
+    // per group (a power of two), experts per lane, and whether every lane's
+    // are whole
+    int wide, run_log2, per, whole;
     int32_t topk;
     int renorm;
     float scale;

@@ -177,10 +177,10 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t i)
     return a.type == W4A8_TYPE_BF16 ? __uint_as_float(h << 16) : half_bits(h);
 }
 
-// logits e0 .. e0 + PL - 1 of a row; -inf behind its end.  a.wide: every row
-// starts at a multiple of 16 bytes and E % PL == 0, so a lane's run is whole.
+// logits e0 .. e0 + count - 1 of a row, then -inf.  a.wide: every row starts at
+// a multiple of 16 bytes, e0 is one of PL, and a lane has PL experts or none.
 template <int PL>
-__device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0, float* x)
+__device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0, int count, float* x)
 {
 #pragma unroll
     for (int i = 0; i < PL; ++i)
@@ -190,9 +190,9 @@ __device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0
         if (!a.wide) {
 #pragma unroll
             for (int i = 0; i < PL; ++i)
-                if (e0 + i < a.E)
+                if (i < count)
                     x[i] = p[i];
-        } else if (e0 < a.E) {
+        } else if (count > 0) {
             if constexpr (PL >= 4) {
 #pragma unroll
                 for (int i = 0; i < PL; i += 4) {
@@ -218,10 +218,10 @@ __device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0
     if (!a.wide) {
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            if (e0 + i < a.E)
+            if (i < count)
                 raw[i / 2] = (i & 1) ? (raw[i / 2] & 0xFFFFu) | (uint32_t)p[i] << 16
                                      : (raw[i / 2] & 0xFFFF0000u) | p[i];
-    } else if (e0 < a.E) {
+    } else if (count > 0) {
         if constexpr (PL >= 8) {
 #pragma unroll
             for (int i = 0; i < PL / 8; ++i) {
@@ -260,7 +260,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t)
     float* const wts = a.weights + t * a.topk;
     const int e0 = lane * PL;
     float x[PL];
-    load_run<PL>(a, t * a.ld, e0, x);
+    load_run<PL>(a, t * a.ld, e0, min(a.E - e0, PL), x);
     uint32_t key[PL];  // of the logit, then of the choice; 0: cannot be chosen
 #pragma unroll
     for (int i = 0; i < PL; ++i)
@@ -447,7 +447,8 @@ __global__ __launch_bounds__(64 * kRWaves) void route_kernel(const RouteArgs a)
 
 // ---- four tokens per wave ------------------------------------------------------------
 //
-// 16 lanes per token, PL consecutive experts each.  The search runs on keys
+// 16 lanes per token, up to PL consecutive experts each; the lanes of a group
+// are a run of 1, 2, 4, 8 or 16, whatever its size.  The search runs on keys
 // of 32 bits that carry the expert's slot in their low bits, so each lane
 // sorts its own with a plain min/max network, and a round is a DPP maximum
 // over the row of 16 lanes that leaves the result in all of them; scores are
@@ -457,7 +458,6 @@ __global__ __launch_bounds__(64 * kRWaves) void route_kernel(const RouteArgs a)
 
 namespace {
 
-constexpr int kRowK = 8;  // most experts per token here
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u(uint32_t v)
@@ -533,7 +533,7 @@ __device__ __forceinline__ void rank_groups(float mine, int l, int run, float sl
 // leave the low 13 or 16 bits of a float free).
 enum RowKey { KEY_CHOICE, KEY_LOGIT32, KEY_LOGIT16 };
 
-template <int PL, int KEY>
+template <int PL, int KEY, int KM>  // KM: most experts per token, 8 or 16
 __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
 {
     constexpr uint32_t kSlots = 15;  // low bits of a key: 15 - slot
@@ -551,10 +551,13 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     const bool live = t < valid;
     const int64_t row = (live ? t : t0) * a.ld;
 
-    const int e0 = l * PL;
+    const int size = a.E / a.groups, run = 1 << a.run_log2;
+    auto first_of = [&](int w) { return (w >> a.run_log2) * size + (w & (run - 1)) * a.per; };
+    const int e0 = first_of(l);
+    const int count = l >> a.run_log2 < a.groups ? min(size - (l & (run - 1)) * a.per, a.per) : 0;
     float x[PL];
     if (live) {
-        load_run<PL>(a, row, e0, x);
+        load_run<PL>(a, row, e0, count, x);
     } else {
 #pragma unroll
         for (int i = 0; i < PL; ++i)
@@ -583,9 +586,10 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     }
     // choices in fp32, off by at most `off` + 2^-23 of their value: the
     // sigmoid's product, exp2, sum and reciprocal cost 2^-22 (kept: 2^-21), the
-    // softmax's sum of up to 20 roundings 2^-19.7 of its terms
+    // softmax's sum of up to 20 roundings 2^-19.7 of its terms, the largest of
+    // which is 1 / sum (kept: 2^-19 of that)
     const bool sums = a.groups > 1 && a.group_top == 2;
-    const float off = a.softmax ? 0x1p-19f : 0x1p-21f;
+    float off = 0x1p-21f;
     uint32_t key[PL], gkey[PL];  // of the experts' order, and of the groups'
     if (KEY == KEY_CHOICE || sums) {
         float c[PL];
@@ -597,6 +601,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
                 sum += c[i];
             }
             const float inv = __builtin_amdgcn_rcpf(row_sum16(sum));
+            off = 0x1p-19f * inv;
 #pragma unroll
             for (int i = 0; i < PL; ++i)
                 c[i] *= inv;
@@ -610,8 +615,8 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
 #pragma unroll
             for (int i = 0; i < PL; ++i)
                 b[i] = 0.0f;
-            if (a.E % PL == 0) {
-                if (e0 < a.E) {
+            if (a.whole) {
+                if (count > 0) {
 #pragma unroll
                     for (int i = 0; i < PL; i += 4) {
                         const float4 v = *(const float4*)(a.bias + e0 + i);
@@ -621,7 +626,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
             } else {
 #pragma unroll
                 for (int i = 0; i < PL; ++i)
-                    if (e0 + i < a.E)
+                    if (i < count)
                         b[i] = a.bias[e0 + i];
             }
         }
@@ -645,7 +650,6 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     bool close = false;  // some pair of the row is too close for 32 bits
     bool open = true;    // the lane's group stays
     if (a.groups > 1) {
-        const int run = a.E / a.groups / PL;  // lanes of a group, a power of two
         uint32_t b1 = gkey[0], b2 = kNoKey;
 #pragma unroll
         for (int i = 1; i < PL; ++i) {
@@ -684,7 +688,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     key[0] = open ? key[0] : 0;  // this lane never holds the largest
     uint32_t mine = 0, lanes_lo = 0, lanes_hi = 0;  // lane j: key j, and which lanes held it
 #pragma unroll
-    for (int j = 0; j < kRowK; ++j) {
+    for (int j = 0; j < KM; ++j) {
         if (j == a.topk)
             break;
         const uint32_t m = row_max(key[0]);
@@ -694,12 +698,12 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
         lanes_lo = l == j ? (uint32_t)lanes : lanes_lo;
         lanes_hi = l == j ? (uint32_t)(lanes >> 32) : lanes_hi;
 #pragma unroll
-        for (int i = 0; i < kRowK - j && i < PL; ++i)
+        for (int i = 0; i < KM - j && i < PL; ++i)
             key[i] = won ? (i + 1 < PL ? key[i + 1] : 0) : key[i];
     }
     const uint32_t rest = row_max(key[0]);  // the best that is not chosen
-    mine = l == a.topk ? rest : mine;
-    const uint32_t next = dpp_u<0x101>(mine);  // row_shl: of lane l + 1
+    const uint32_t after = dpp_u<0x101>(mine);  // row_shl: of lane l + 1
+    const uint32_t next = l + 1 == a.topk ? rest : after;
     const bool chosen = l < a.topk && mine > kNoKey;
     bool near = false;  // too close to the next one for the keys to tell
     if (KEY != KEY_LOGIT16 && chosen && next > kNoKey) {
@@ -716,7 +720,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     if (chosen) {
         const uint32_t lanes = ((lane & 32 ? lanes_hi : lanes_lo) >> (lane & 16)) & 0xFFFF;
         my_id = KEY == KEY_LOGIT16 ? (int)(0xFF - (mine & 0xFF))
-                                   : (__ffs((int)lanes) - 1) * PL + (int)(kSlots - (mine & kSlots));
+                                   : first_of(__ffs((int)lanes) - 1) + (int)(kSlots - (mine & kSlots));
         close |= KEY != KEY_LOGIT16 && (lanes & (lanes - 1)) != 0;  // one key in several lanes: all gave it up
         const float v = load_logit(a, row + my_id);
         s = a.softmax ? exp_below64(v, top) : sigmoid64(v);
@@ -725,12 +729,23 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     if (KEY != KEY_LOGIT16 && __ballot(near) != 0) {
         // two chosen ones that 64 bits find in order are fine; the last chosen
         // one against all the others is not known that way
-        if (KEY == KEY_CHOICE && chosen)
-            exact = s + (double)a.bias[my_id];
+        if (KEY == KEY_CHOICE) {
+            double whole = total;
+            if (a.softmax && a.renorm) {  // not needed so far, and seldom here
+                float again[PL];
+                load_run<PL>(a, row, e0, live ? count : 0, again);
+                whole = 0.0;
+#pragma unroll
+                for (int i = 0; i < PL; ++i)
+                    whole += again[i] > ninf ? exp_below64(again[i], top) : 0.0;
+                whole = run_sum<0>(whole, 16);
+            }
+            if (chosen)
+                exact = (a.softmax ? s / whole : s) + (double)a.bias[my_id];
+        }
         const double other = dpp_d<0x101>(exact);
         const int other_id = (int)dpp_u<0x101>((uint32_t)my_id);
-        const bool ordered = l + 1 < a.topk && (KEY == KEY_LOGIT32 || !a.softmax) &&
-                             (exact > other || (exact == other && my_id < other_id));
+        const bool ordered = l + 1 < a.topk && (exact > other || (exact == other && my_id < other_id));
         close |= near && !ordered;
     }
     if (a.renorm) {
@@ -776,45 +791,52 @@ void launch_lanes(const RouteArgs& a, bool scores, hipStream_t s)
 
 namespace {
 
-// rows of 16 lanes: up to 8 of up to 256 experts, groups that are runs of
-// 1, 2, 4 or 8 lanes
-template <int PL>
-bool row_groups(const RouteArgs& a)
-{
-    const int size = a.E / a.groups, run = size / PL;
-    return a.groups == 1 || (run * PL == size && run >= 1 && run <= 8 && (run & (run - 1)) == 0);
-}
-template <int PL>
+template <int PL, int KM>
 void launch_rows(const RouteArgs& a, hipStream_t s)
 {
-    RouteArgs b = a;
-    b.wide = (a.ld * (a.type == W4A8_TYPE_FP32 ? 4 : 2)) % 16 == 0 && a.E % PL == 0;
     // few tokens: a wave per workgroup, so that they spread over the CUs
     const int waves = a.T <= 4096 ? 1 : 4;
     const dim3 grid((unsigned)((a.T + 4 * waves - 1) / (4 * waves))), block(64 * waves);
     if (a.bias != nullptr)
-        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_CHOICE>), grid, block, 0, s, b);
+        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_CHOICE, KM>), grid, block, 0, s, a);
     else if (a.type == W4A8_TYPE_FP32)
-        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_LOGIT32>), grid, block, 0, s, b);
+        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_LOGIT32, KM>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_LOGIT16>), grid, block, 0, s, b);
+        hipLaunchKernelGGL((route_rows_kernel<PL, KEY_LOGIT16, KM>), grid, block, 0, s, a);
+}
+
+// rows of 16 lanes: up to 16 experts of at most 16 groups, each of which gets
+// the lanes of a power of two and fits them with 16 experts a lane
+template <int PL>
+bool try_rows(RouteArgs a, int per, int run_log2, hipStream_t s)
+{
+    if (per > PL)
+        return false;
+    const int size = a.E / a.groups;
+    a.per = a.groups == 1 ? PL : per;
+    a.run_log2 = run_log2;
+    a.whole = a.per == PL && size % PL == 0;
+    a.wide = a.whole && (a.ld * (a.type == W4A8_TYPE_FP32 ? 4 : 2)) % 16 == 0;
+    if (a.topk <= 8)
+        launch_rows<PL, 8>(a, s);
+    else
+        launch_rows<PL, 16>(a, s);
+    return true;
 }
 
 }  // namespace
 
+// Four tokens per wave where their rows fit 16 lanes, else one (32768 tokens,
+// 256 experts in 8 groups, top 8: 20 us against 52).
 hipError_t launch_route(const RouteArgs& a, hipStream_t s)
 {
-    if (a.topk <= kRowK && a.E <= 256) {
-        const bool p4 = a.E <= 64, p8 = a.E <= 128;
-        if (p4 ? row_groups<4>(a) : p8 ? row_groups<8>(a) : row_groups<16>(a)) {
-            if (p4)
-                launch_rows<4>(a, s);
-            else if (p8)
-                launch_rows<8>(a, s);
-            else
-                launch_rows<16>(a, s);
+    if (a.topk <= 16 && a.groups <= 16) {
+        int run_log2 = 4;
+        while ((16 >> run_log2) < a.groups)
+            --run_log2;
+        const int lanes = 1 << run_log2, per = (a.E / a.groups + lanes - 1) / lanes;
+        if (try_rows<4>(a, per, run_log2, s) || try_rows<8>(a, per, run_log2, s) || try_rows<16>(a, per, run_log2, s))
             return hipGetLastError();
-        }
     }
     const bool scores =
         a.bias != nullptr || (a.groups > 1 && a.group_top == 2) || (a.softmax && !a.renorm);
