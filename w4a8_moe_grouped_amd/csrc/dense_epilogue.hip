@@ -13,6 +13,9 @@
 // kept a CU's address unit busy for 4.5 us of a 12 us call.)  The 8 sums of
 // an output meet in LDS, in wave order.
 //
+// M 1, K 7168, R 4096: 7.0 us for 15.6 MB (2.2 TB/s; 4.1 us of it at K = 128:
+// launch, one load, the sums); M 64, K 2048, R 7168 with a residual: 7.0 us.
+//
 // The weights are the first MFMA operand, so a lane holds four consecutive
 // outputs of one row, which the epilogue reads and writes as one access.  With
 // SwiGLU, fragment f of the up rows stands beside fragment f of the gate rows.

@@ -9,7 +9,10 @@
 // accesses of a wave are contiguous and the 16 chunks of a 128-block, whose
 // largest value sets its scale, lie in 16 neighbouring lanes.  Short rows take
 // one wave each (no barrier), longer ones a workgroup each.  Sums and the
-// values between them are fp32.
+// values between them are fp32.  Measured at H = 7168: 4096 rows of bf16 to
+// codes 46 us (4.5 TB/s of the 5.1 a copy reaches; loads and stores past the
+// caches changed nothing), 16384 rows with an fp32 residual 262 us (5.4 TB/s),
+// 64 rows 5.2 us, one row 3.4 us (two dependent sums behind one load: latency).
 #include "w4a8.h"
 
 #include "common.hpp"

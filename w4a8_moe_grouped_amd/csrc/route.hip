@@ -1,20 +1,31 @@
-// route.hip -- router scores to expert ids and weights (w4a8_moe_route).
+// route.hip -- router scores to expert ids and weights (w4a8_moe_route):
+//   s = sigmoid(x) or softmax(x),  c = s + bias,  groups by the sum of their two
+//   best c,  the k best c of the groups kept,  weights scale * s / sum of s.
 //
-// One wave per token.  Lane l holds the PL consecutive experts l*PL .. l*PL +
-// PL - 1, so a row is one coalesced load and the lower index of equal values
-// is in the lower lane, or in the lower slot of one lane.
+// Which experts are chosen, and in which order, is decided by 64-bit values,
+// since differences of scores that 32 bits round away still order the
+// experts.  But few tokens need that many bits, so the search runs in 32: the
+// fast kernel (route_rows_kernel, four tokens per wave) bounds the error of its
+// choices and hands the tokens it cannot decide to the exact one (route_token,
+// one token per wave, also for more experts or groups than fit 16 lanes).
+// There, too, the search runs on 32-bit keys: the choice rounded to fp32 is
+// monotone in it, so the largest key belongs to the largest choice unless
+// several experts share it, and only then (a wave-uniform branch) are the
+// 64-bit values compared.  Without a bias the logits order the scores, and the
+// key is the logit itself.  The scores of the chosen are evaluated once more in
+// 64 bits, one per lane, and rounded once.
 //
-// Which experts are chosen is decided by 64-bit values, since differences of
-// scores that 32 bits round away still order the experts; but the search runs
-// on 32-bit keys: the choice rounded to fp32 is monotone in it, so the largest
-// key belongs to the largest choice unless several experts share it, and only
-// then (a wave-uniform branch) are the 64-bit values compared.  Without a bias
-// the logits order the scores, and the key is the logit itself.  A round of
-// the search is one DPP maximum over the wave (no LDS) and one ballot per
-// slot.  The scores of the chosen are evaluated once more, one per lane.
+// In the exact kernel lane l holds the PL consecutive experts l*PL .. l*PL + PL
+// - 1, so a row is one coalesced load and the lower index of equal values is in
+// the lower lane, or in the lower slot of one lane; a round of the search is a
+// DPP maximum over the wave (no LDS) and one ballot per slot.
 //
-// Bound: instruction issue (about 300 a token with 256 experts in groups,
-// 100 of them the 64-bit sigmoids), not the 4 E bytes read per token.
+// Bound: instruction issue.  32768 tokens, 256 experts in 8 groups, top 8,
+// sigmoid and bias: 20 us, 1.8 TB/s of logits; 190 vector operations a token
+// (765 per wave of four), which alone are 10.5 us of every SIMD; the exact kernel
+// takes 52 us.  How many waves a CU holds does not matter (12 to 24: 20.4 to
+// 22.8 us), nor does loading the next tokens ahead.  64 tokens: 5 us, all
+// latency.
 #include "w4a8.h"
 
 #include "common.hpp"
@@ -510,6 +521,30 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N])
                     }
 }
 
+// Rounds J .. topk - 1 of the search, unrolled (a loop left rolled indexes the
+// keys at run time: 2.5 us a round): lane J of each row gets the row's largest
+// key and the lanes that held it, and these move on to their next.
+template <int J, int KM, int PL>
+__device__ __forceinline__ void take_best(uint32_t (&key)[PL], int topk, int l, uint32_t& mine, uint32_t& lanes_lo,
+                                          uint32_t& lanes_hi)
+{
+    if constexpr (J < KM) {
+        if (J == topk)
+            return;
+        const uint32_t m = row_max(key[0]);
+        const bool won = key[0] == m;
+        const uint64_t lanes = __ballot(won);
+        mine = l == J ? m : mine;
+        lanes_lo = l == J ? (uint32_t)lanes : lanes_lo;
+        lanes_hi = l == J ? (uint32_t)(lanes >> 32) : lanes_hi;
+        // as far as later rounds can ask for them
+#pragma unroll
+        for (int i = 0; i < KM - J && i < PL; ++i)
+            key[i] = won ? (i + 1 < PL ? key[i + 1] : 0) : key[i];
+        take_best<J + 1, KM>(key, topk, l, mine, lanes_lo, lanes_hi);
+    }
+}
+
 // other groups of the row, one rotation after another (lane l reads l - N, a
 // lower group unless that wraps): how many are better than this lane's, and
 // whether any is too close to tell
@@ -687,20 +722,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     sort_down(key);
     key[0] = open ? key[0] : 0;  // this lane never holds the largest
     uint32_t mine = 0, lanes_lo = 0, lanes_hi = 0;  // lane j: key j, and which lanes held it
-#pragma unroll
-    for (int j = 0; j < KM; ++j) {
-        if (j == a.topk)
-            break;
-        const uint32_t m = row_max(key[0]);
-        const bool won = key[0] == m;
-        const uint64_t lanes = __ballot(won);
-        mine = l == j ? m : mine;
-        lanes_lo = l == j ? (uint32_t)lanes : lanes_lo;
-        lanes_hi = l == j ? (uint32_t)(lanes >> 32) : lanes_hi;
-#pragma unroll
-        for (int i = 0; i < KM - j && i < PL; ++i)
-            key[i] = won ? (i + 1 < PL ? key[i + 1] : 0) : key[i];
-    }
+    take_best<0, KM>(key, a.topk, l, mine, lanes_lo, lanes_hi);
     const uint32_t rest = row_max(key[0]);  // the best that is not chosen
     const uint32_t after = dpp_u<0x101>(mine);  // row_shl: of lane l + 1
     const uint32_t next = l + 1 == a.topk ? rest : after;
