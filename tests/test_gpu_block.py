@@ -300,6 +300,22 @@ def test_norm_empty(dev):
         assert out.shape == y.shape == (0, 256)
 
 
+def test_norm_both_outputs_through_the_c_abi(dev):
+    """bf16 and codes of one call are those of the two separate calls."""
+    L, T, H = w4.load(), 37, 1024
+    d = norm_inputs(dev, T, H, BF16, BF16, FP32)
+    kw = dict(post_weight=d["post"], pre_weight=d["pre"], residual_scale=0.5)
+    r, y, _ = w4.norm_residual(d["x"], d["residual"], **kw)
+    _, q, s = w4.norm_residual(d["x"], d["residual"], quantize=True, **kw)
+    r2, y2, q2, s2 = (torch.full_like(t, 1) for t in (r, y, q, s))
+    p = lambda t: t.data_ptr()  # noqa: E731
+    assert L.w4a8_norm_residual(p(d["x"]), 1, H, p(d["residual"]), 1, H, T, H, 0, p(d["post"]), None, 0, 0, 0.5, p(d["pre"]),
+                                0.0, 1e-6, p(r2), H, p(y2), H, p(q2), p(s2),
+                                torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in ((r, r2), (y, y2), (q, q2), (s, s2)))
+
+
 def test_norm_codes_are_quantize_act_of_the_same_values(dev):
     """Rows whose normed values are bf16 numbers: the codes and scales are
     those of quantize_act on them, bit for bit."""
