@@ -466,7 +466,7 @@ int w4a8_fused_moe_prepacked_noalloc(const void* hidden_bf16, int64_t T, int64_t
  *   topk_ids     [T, topk] int32;  topk_weights [T, topk] fp32
  * T >= 0 (T == 0 launches nothing), 1 <= topk <= 32, topk <= topk_groups *
  * E/num_groups, 1 <= topk_groups <= num_groups, num_groups divides E
- * (INVALID_ARG otherwise); E <= 1024, T < 2^31, num_groups <= 64, num_tokens
+ * (INVALID_ARG otherwise); E <= 1024, T <= 2^25, num_groups <= 64, num_tokens
  * 4-byte aligned, pointers 16-byte aligned (UNSUPPORTED otherwise).  Any row
  * stride; rows of 16-byte aligned start and length are read with wide loads.
  */
@@ -506,8 +506,8 @@ int w4a8_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, in
  * T >= 0 (T == 0 launches nothing), H > 0, eps >= 2^-126; pre_weight and an output
  * of y go together, and so do a missing pre_weight and none; x or residual
  * must be given, and some output; post_weight and gate need x (INVALID_ARG
- * otherwise).  H <= 32768, T < 2^31, H % 128 == 0 with codes, pointers
- * 16-byte aligned (UNSUPPORTED otherwise).  Any row strides >= H; rows whose
+ * otherwise).  H <= 32768, T < 2^22 (T <= 2^25 where H <= 512), H % 128 == 0
+ * with codes, pointers 16-byte aligned (UNSUPPORTED otherwise).  Any row strides >= H; rows whose
  * start is 16-byte aligned are read and written with wide accesses.  Squares
  * are summed in fp32: |values| stay below 2^56.
  */
@@ -534,8 +534,9 @@ int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* resid
  *   workspace    device scratch of *workspace_bytes bytes (query with NULL; it
  *                depends on M, K, N and activation alone, and may be 0)
  * M >= 0 (M == 0 launches nothing), N > 0, K > 0 (INVALID_ARG otherwise), K %
- * 128 == 0, K <= 2^22, M, R < 2^31, ceil(M/32) * ceil(N/16) < 2^31, pointers
- * 16-byte aligned (UNSUPPORTED otherwise).  Operands may exceed 2^32 bytes.
+ * 128 == 0, K <= 2^22, M, R < 2^31, launches below 2^32 threads (met by up to
+ * 2^33 outputs with M % 32 == 0 and 2^36 weights), pointers 16-byte aligned
+ * (UNSUPPORTED otherwise).  Operands may exceed 2^32 bytes.
  */
 #define W4A8_ACT_NONE 0
 #define W4A8_ACT_RELU 1

@@ -67,6 +67,16 @@ def test_norm_arguments(L, change, want):
     assert _norm(L, **change) == want
 
 
+@pytest.mark.parametrize("T, H, want", [(1 << 22, 520, UNSUPPORTED), ((1 << 25) + 1, 512, UNSUPPORTED)])
+def test_norm_rows_of_one_launch(L, T, H, want):
+    """A launch holds less than 2^32 threads."""
+    assert _norm(L, T=T, H=H, ldx=H, ldr=H, ldo=H, ldy=H) == want
+
+
+def test_route_tokens_of_one_launch(L):
+    assert _route(L, T=(1 << 25) + 1) == UNSUPPORTED
+
+
 def _gemm(L, a=P, sa=P, M=0, K=256, b=P, sb=P, N=64, bias=None, bt=0, act=0, res=None, ldr=64, out=P2, ldo=64, ws=P,
           nbytes=1 << 50):
     n = ctypes.c_size_t(nbytes)
@@ -146,3 +156,15 @@ def test_ref_gemm_is_the_oracle(orc):
     t = torch.from_numpy
     got, _ = ref.gemm_epilogue(t(codes), t(sa), t(w), t(sw))
     np.testing.assert_allclose(got.numpy(), orc.gemm_f64(codes, sa, w, sw), rtol=1e-12, atol=1e-9)
+
+
+@pytest.mark.parametrize("M, K, N, act, want", [
+    # 128 x 128 tiles of 256 threads: 8192 x 257
+    (1 << 20, 128, 1 << 13, 5, OK), (1 << 20, 128, (1 << 14) + 32, 5, OK),
+    # 512 threads for 32 weight rows; 256 threads for 32 rows x 64 weight rows
+    (16, 128, (1 << 28) + 32, 0, UNSUPPORTED), (17, 128, (1 << 30) + 64, 0, UNSUPPORTED), (17, 128, 1 << 29, 0, OK),
+    # the first pass: 256 threads for 8192 weights
+    (1 << 13, 4096, 1 << 13, 0, OK), (1 << 17, 1 << 20, 1 << 18, 0, UNSUPPORTED)])
+def test_gemm_epilogue_threads_of_one_launch(L, M, K, N, act, want):
+    """Both kernels' launches hold less than 2^32 threads; the query says so."""
+    assert _gemm(L, M=M, K=K, N=N, act=act, ldo=N, ws=None) == want

@@ -663,6 +663,14 @@ def test_two_streams_at_once(dev, M, K, N):
             assert all(torch.equal(a, b) for a, b in zip(one, want[k]))
 
 
+def test_binding_refuses_a_workspace_with_holes_and_a_cut_group_top(dev):
+    ops = gemm_inputs(dev, 2100, 7168, 1024)
+    with pytest.raises(w4.W4A8Error, match="contiguous"):
+        w4.gemm_epilogue(*ops, workspace=torch.zeros(16, 1, dtype=torch.uint8, device=dev).expand(16, 4096))
+    with pytest.raises(w4.W4A8Error):
+        w4.moe_route(torch.zeros(4, 16, device=dev), 4, group_top=2 + 2 ** 32)
+
+
 def test_binding_checks_on_the_gpu(dev):
     x = torch.zeros(4, 256, dtype=BF16, device=dev)
     w = torch.ones(256, device=dev)

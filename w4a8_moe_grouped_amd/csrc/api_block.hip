@@ -16,6 +16,9 @@ using namespace w4a8::api;
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxGroups = 64;
 constexpr int64_t kMaxDenseK = (int64_t)1 << 22;
+// a launch holds less than 2^32 threads: up to 64 a token, a short row; 1024 a row
+constexpr int64_t kMaxTokens = (int64_t)1 << 25;
+constexpr int64_t kMaxLongRows = ((int64_t)1 << 22) - 1;
 
 inline bool float_or_bf16(int type)
 {
@@ -43,7 +46,7 @@ int w4a8_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, in
     if ((logits_type != W4A8_TYPE_FP32 && logits_type != W4A8_TYPE_BF16 && logits_type != W4A8_TYPE_FP16) ||
         (score != W4A8_SCORE_SIGMOID && score != W4A8_SCORE_SOFTMAX) || (group_top != 1 && group_top != 2))
         return W4A8_ERR_INVALID_ARG;
-    if (topk > W4A8_MAX_TOPK || E > kMaxExperts || num_groups > kMaxGroups || T > INT32_MAX)
+    if (topk > W4A8_MAX_TOPK || E > kMaxExperts || num_groups > kMaxGroups || T > kMaxTokens)
         return W4A8_ERR_UNSUPPORTED;
     if (T > 0 && (logits == nullptr || topk_ids == nullptr || topk_weights == nullptr))
         return W4A8_ERR_INVALID_ARG;
@@ -99,7 +102,7 @@ int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* resid
         return W4A8_ERR_INVALID_ARG;
     if (residual_out != nullptr && residual_out == residual && ldr_out != ldr)
         return W4A8_ERR_INVALID_ARG;
-    if (H > w4a8::kNormMaxH || T > INT32_MAX || (q_e4m3 != nullptr && H % W4A8_GROUP != 0))
+    if (H > w4a8::kNormMaxH || T > (H <= w4a8::kNormShortH ? kMaxTokens : kMaxLongRows) || (q_e4m3 != nullptr && H % W4A8_GROUP != 0))
         return W4A8_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(residual) || !aligned16(post_weight) || !aligned16(gate) ||
         !aligned16(pre_weight) || !aligned16(residual_out) || !aligned16(y_bf16) || !aligned16(q_e4m3) ||
@@ -149,8 +152,7 @@ int w4a8_gemm_epilogue(const uint8_t* a_e4m3, const float* a_scales, int64_t M, 
     if (K % W4A8_GROUP != 0 || K > kMaxDenseK || M > INT32_MAX ||
         mul_sat(N, activation == W4A8_ACT_SWIGLU ? 2 : 1) > INT32_MAX)
         return W4A8_ERR_UNSUPPORTED;
-    // workgroups of 32 rows x at least 16 outputs
-    if (mul_sat(ceil_div(M, 32), ceil_div(N, 16)) > INT32_MAX)
+    if (mul_sat(ceil_div(M, 32), ceil_div(N, 16)) > INT32_MAX || !w4a8::dense_epilogue_fits(M, K, N, activation))
         return W4A8_ERR_UNSUPPORTED;
     const size_t need = w4a8::dense_epilogue_workspace(M, K, N, activation);
     const int ws_rc = check_workspace(workspace, workspace_bytes, need);

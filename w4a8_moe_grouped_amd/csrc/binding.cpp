@@ -240,8 +240,9 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n)
             made_w = make({T, k}, at::kFloat, device), w = &made_w;
         const int type = type_of(logits, true);
         const int64_t ld = row_stride(logits, T, E, "logits");
-        const int score = (int)integer(a[2]), top = (int)integer(a[6]);
-        const int64_t groups = integer(a[4]), kept = integer(a[5]);
+        const int score = (int)integer(a[2]);
+        const int64_t groups = integer(a[4]), kept = integer(a[5]), group_top = integer(a[6]);
+        const int top = group_top == 1 || group_top == 2 ? (int)group_top : 0;  // 0: refused
         const int renorm = truth(a[7]);
         const float scale = number(a[8]);
         const void* x = logits.data_ptr();
@@ -425,6 +426,8 @@ PyObject* gemm_epilogue(PyObject*, PyObject* const* a, Py_ssize_t n)
                 if (bytes > 0)
                     made_ws = make({(int64_t)bytes}, at::kByte, device), ws = &made_ws;
             } else {
+                if (!ws->is_contiguous())
+                    refuse("workspace must be contiguous");
                 bytes = ws->numel() * ws->element_size();
             }
             // a call that needs none still names a buffer (null asks for the size)

@@ -19,6 +19,7 @@
 // The weights are the first MFMA operand, so a lane holds four consecutive
 // outputs of one row, which the epilogue reads and writes as one access.  With
 // SwiGLU, fragment f of the up rows stands beside fragment f of the gate rows.
+#include "api_util.hpp"
 #include "dense_common.hpp"
 #include "lds_direct.hpp"
 
@@ -267,6 +268,17 @@ hipError_t launch_rows(const DenseArgs& a, hipStream_t s)
 size_t dense_epilogue_workspace(int64_t M, int64_t K, int64_t N, int act)
 {
     return use_dense_tiles(M, K, N, act) ? dense_tiles_workspace(M, K, N, act) : 0;
+}
+
+// Whether every launch of the call stays below 2^32 threads; the choices are
+// those of launch_dense_epilogue (few workgroups always do).
+bool dense_epilogue_fits(int64_t M, int64_t K, int64_t N, int act)
+{
+    if (use_dense_tiles(M, K, N, act))
+        return dense_tiles_fit(M, K, N, act);
+    const int64_t R = act == W4A8_ACT_SWIGLU ? 2 * N : N;
+    const int64_t threads = M <= 16 ? api::ceil_div(R, 32) * 512 : api::ceil_div(M, 32) * api::ceil_div(R, 64) * 256;
+    return threads <= UINT32_MAX;
 }
 
 hipError_t launch_dense_epilogue(const DenseArgs& a, void* ws, hipStream_t s)

@@ -349,12 +349,26 @@ TileArgs plan_tiles(void* ws, const DenseArgs& d, size_t* bytes)
     return t;
 }
 
+// workgroups of the first pass
+int64_t expand_blocks(const TileArgs& t)
+{
+    return 4 * (int64_t)t.units_n * ((t.G + 1) / 2) + ((int64_t)t.units_n + t.units_m) * ((t.G + 7) / 8);
+}
+
+// tiles along both axes; their workgroups, a multiple of the 8 XCDs
+template <typename L>
+int64_t tile_blocks(const TileArgs& t, int64_t& tiles_m, int64_t& tiles_n)
+{
+    tiles_m = api::ceil_div(t.units_m, L::kBM / kUnit), tiles_n = api::ceil_div(t.units_n, L::kBN / kUnit);
+    return (tiles_m * tiles_n + 7) / 8 * 8;
+}
+
 template <int WM, int WN, int SL>
 hipError_t launch_tiles(const TileArgs& t, hipStream_t s)
 {
     using L = Tile<WM, WN, SL>;
-    const int64_t tiles_m = api::ceil_div(t.units_m, L::kBM / kUnit), tiles_n = api::ceil_div(t.units_n, L::kBN / kUnit);
-    const dim3 grid((unsigned)((tiles_m * tiles_n + 7) / 8 * 8));
+    int64_t tiles_m, tiles_n;
+    const dim3 grid((unsigned)tile_blocks<L>(t, tiles_m, tiles_n));
     hipLaunchKernelGGL((dense_tile_kernel<WM, WN, SL>), grid, dim3(L::kThreads), 0, s, t, (int32_t)tiles_m,
                        (int32_t)tiles_n);
     return hipGetLastError();
@@ -413,14 +427,23 @@ size_t dense_tiles_workspace(int64_t M, int64_t K, int64_t N, int act)
     return bytes;
 }
 
+// the first pass has 256 threads a workgroup, the small tiles as many and
+// four times the large ones' workgroups
+bool dense_tiles_fit(int64_t M, int64_t K, int64_t N, int act)
+{
+    DenseArgs d = {};
+    d.M = M, d.K = K, d.N = N, d.act = act;
+    size_t bytes;
+    int64_t m, n;
+    const TileArgs t = plan_tiles(nullptr, d, &bytes);
+    return expand_blocks(t) * 256 <= UINT32_MAX && tile_blocks<Tile<2, 2, 4>>(t, m, n) * 256 <= UINT32_MAX;
+}
+
 hipError_t launch_dense_tiles(const DenseArgs& d, void* ws, hipStream_t s)
 {
     size_t bytes;
     const TileArgs t = plan_tiles(ws, d, &bytes);
-    const int64_t blocks = 4 * (int64_t)t.units_n * ((t.G + 1) / 2) + (int64_t)(t.units_n + t.units_m) * ((t.G + 7) / 8);
-    if (blocks > INT32_MAX)
-        return hipErrorInvalidValue;
-    hipLaunchKernelGGL(dense_expand_kernel, dim3((unsigned)blocks), dim3(256), 0, s, t);
+    hipLaunchKernelGGL(dense_expand_kernel, dim3((unsigned)expand_blocks(t)), dim3(256), 0, s, t);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;

@@ -244,6 +244,7 @@ struct NormArgs {
     int aligned;  // every row starts at a multiple of 16 bytes
 };
 constexpr int64_t kNormMaxH = 32768;
+constexpr int kNormShortH = 512;  // up to here a wave holds a row
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 
 // ---- dense linear with an epilogue (dense_epilogue.hip) ----
@@ -265,11 +266,13 @@ struct DenseArgs {
     int vec4, vec2;
 };
 size_t dense_epilogue_workspace(int64_t M, int64_t K, int64_t N, int act);
+bool dense_epilogue_fits(int64_t M, int64_t K, int64_t N, int act);
 hipError_t launch_dense_epilogue(const DenseArgs& a, void* ws, hipStream_t s);
 // many rows (dense_tiles.hip): from which sizes on, and the workspace of its
 // expanded weights
 bool use_dense_tiles(int64_t M, int64_t K, int64_t N, int act);
 size_t dense_tiles_workspace(int64_t M, int64_t K, int64_t N, int act);
+bool dense_tiles_fit(int64_t M, int64_t K, int64_t N, int act);
 hipError_t launch_dense_tiles(const DenseArgs& a, void* ws, hipStream_t s);
 
 } // namespace w4a8

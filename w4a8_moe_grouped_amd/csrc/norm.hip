@@ -248,7 +248,7 @@ void launch_typed(const NormArgs& a, hipStream_t s)
 {
     const int chunks = (a.H + 7) / 8;
     const unsigned T = (unsigned)a.T;
-    if (chunks <= 64) {
+    if (a.H <= kNormShortH) {
         hipLaunchKernelGGL((norm_kernel<XT, RT, 1, true, VEC>), dim3((T + kNRows - 1) / kNRows),
                            dim3(64 * kNRows), 0, s, a);
         return;
