@@ -507,9 +507,8 @@ int w4a8_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, in
  * of y go together, and so do a missing pre_weight and none; x or residual
  * must be given, and some output; post_weight and gate need x (INVALID_ARG
  * otherwise).  H <= 32768, T < 2^22 (T <= 2^25 where H <= 512), H % 128 == 0
- * with codes, pointers 16-byte aligned (UNSUPPORTED otherwise).  Any row strides >= H; rows whose
- * start is 16-byte aligned are read and written with wide accesses.  Squares
- * are summed in fp32: |values| stay below 2^56.
+ * with codes, pointers 16-byte aligned (UNSUPPORTED otherwise).  Any row
+ * strides >= H.  Squares are summed in fp32: |values| stay below 2^56.
  */
 int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* residual,
                        int residual_type, int64_t ldr, int64_t T, int64_t H, int param_type,

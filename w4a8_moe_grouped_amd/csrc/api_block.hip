@@ -24,11 +24,6 @@ inline bool float_or_bf16(int type)
 {
     return type == W4A8_TYPE_FP32 || type == W4A8_TYPE_BF16;
 }
-// a row stride keeps 16-byte alignment for elements of this type
-inline bool stride16(int64_t ld, int type)
-{
-    return ld % (type == W4A8_TYPE_FP32 ? 4 : 8) == 0;
-}
 
 }  // namespace
 
@@ -134,10 +129,6 @@ int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* resid
     a.y = (uint16_t*)y_bf16;
     a.q = q_e4m3;
     a.q_scales = q_scales;
-    a.aligned = (x == nullptr || stride16(ldx, x_type)) && (residual == nullptr || stride16(ldr, residual_type)) &&
-                (residual_out == nullptr || stride16(ldr_out, residual_type)) &&
-                (y_bf16 == nullptr || stride16(ldy, W4A8_TYPE_BF16)) &&
-                (gate == nullptr || gate_col_stride == 0 || stride16(gate_row_stride, param_type));
     return hip_status(w4a8::launch_norm(a, stream));
 }
 

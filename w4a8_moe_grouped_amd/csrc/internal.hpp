@@ -241,7 +241,6 @@ struct NormArgs {
     uint16_t* y;      // bf16 or null
     uint8_t* q;       // e4m3 codes [T, H] with q_scales [T, H/128], or null
     float* q_scales;
-    int aligned;  // every row starts at a multiple of 16 bytes
 };
 constexpr int64_t kNormMaxH = 32768;
 constexpr int kNormShortH = 512;  // up to here a wave holds a row

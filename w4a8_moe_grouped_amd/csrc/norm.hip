@@ -24,28 +24,33 @@ namespace {
 
 constexpr int kNRows = 4;  // rows per workgroup with one wave per row
 
-template <bool VEC>
+// Rows start at any element, so 16 bytes are accessed at the alignment of one
+// of them; a misaligned wide access is one instruction here (16220 rows of 2085
+// bf16: 51 us, element by element 224).
+typedef float float4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t uint4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 __device__ __forceinline__ void load8(const float* p, int h, int H, float* v)
 {
-    if (VEC && h + 8 <= H) {
-        const float4 a = *(const float4*)(p + h), b = *(const float4*)(p + h + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    if (h + 8 <= H) {
+        const float4_any a = *(const float4_any*)(p + h), b = *(const float4_any*)(p + h + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = a[i], v[4 + i] = b[i];
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         v[i] = h + i < H ? p[h + i] : 0.0f;
 }
-template <bool VEC>
 __device__ __forceinline__ void load8(const uint16_t* p, int h, int H, float* v)
 {
-    if (VEC && h + 8 <= H) {
-        const v4i raw = ldg16(p + h);
+    if (h + 8 <= H) {
+        const uint4_any raw = *(const uint4_any*)(p + h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float((uint32_t)raw[i] << 16);
-            v[2 * i + 1] = __uint_as_float((uint32_t)raw[i] & 0xFFFF0000u);
+            v[2 * i] = __uint_as_float(raw[i] << 16);
+            v[2 * i + 1] = __uint_as_float(raw[i] & 0xFFFF0000u);
         }
         return;
     }
@@ -53,25 +58,23 @@ __device__ __forceinline__ void load8(const uint16_t* p, int h, int H, float* v)
     for (int i = 0; i < 8; ++i)
         v[i] = h + i < H ? bf16_to_f32(p[h + i]) : 0.0f;
 }
-template <bool VEC>
 __device__ __forceinline__ void load8_param(const void* p, int64_t row, int type, int h, int H, float* v)
 {
     if (type == W4A8_TYPE_FP32)
-        load8<VEC>((const float*)p + row, h, H, v);
+        load8((const float*)p + row, h, H, v);
     else
-        load8<VEC>((const uint16_t*)p + row, h, H, v);
+        load8((const uint16_t*)p + row, h, H, v);
 }
 __device__ __forceinline__ float load1_param(const void* p, int64_t i, int type)
 {
     return type == W4A8_TYPE_FP32 ? ((const float*)p)[i] : bf16_to_f32(((const uint16_t*)p)[i]);
 }
 
-template <bool VEC>
 __device__ __forceinline__ void store8(float* p, int h, int H, const float* v)
 {
-    if (VEC && h + 8 <= H) {
-        *(float4*)(p + h) = make_float4(v[0], v[1], v[2], v[3]);
-        *(float4*)(p + h + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    if (h + 8 <= H) {
+        *(float4_any*)(p + h) = float4_any{v[0], v[1], v[2], v[3]};
+        *(float4_any*)(p + h + 4) = float4_any{v[4], v[5], v[6], v[7]};
         return;
     }
 #pragma unroll
@@ -79,15 +82,14 @@ __device__ __forceinline__ void store8(float* p, int h, int H, const float* v)
         if (h + i < H)
             p[h + i] = v[i];
 }
-template <bool VEC>
 __device__ __forceinline__ void store8(uint16_t* p, int h, int H, const float* v)
 {
     uint32_t d[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         d[i] = f32x2_to_bf16x2(v[2 * i], v[2 * i + 1]);
-    if (VEC && h + 8 <= H) {
-        *(uint4*)(p + h) = make_uint4(d[0], d[1], d[2], d[3]);
+    if (h + 8 <= H) {
+        *(uint4_any*)(p + h) = uint4_any{d[0], d[1], d[2], d[3]};
         return;
     }
 #pragma unroll
@@ -124,7 +126,7 @@ __device__ __forceinline__ float row_sum(float v, float* s_part)
 
 }  // namespace
 
-template <typename XT, typename RT, int NC, bool WAVE_ROW, bool VEC>
+template <typename XT, typename RT, int NC, bool WAVE_ROW>
 __global__ __launch_bounds__(WAVE_ROW ? 64 * kNRows : 1024) void norm_kernel(const NormArgs a)
 {
     __shared__ float s_part[2][16];
@@ -141,9 +143,9 @@ __global__ __launch_bounds__(WAVE_ROW ? 64 * kNRows : 1024) void norm_kernel(con
     for (int c = 0; c < NC; ++c) {
         const int h = (c * threads + tid) * 8;
         if (a.x != nullptr)
-            load8<VEC>((const XT*)a.x + t * a.ldx, h, H, v[c]);
+            load8((const XT*)a.x + t * a.ldx, h, H, v[c]);
         if (a.residual != nullptr)
-            load8<VEC>((const RT*)a.residual + t * a.ldr, h, H, r[c]);
+            load8((const RT*)a.residual + t * a.ldr, h, H, r[c]);
     }
     // r' in v
     if (a.x != nullptr) {
@@ -164,13 +166,13 @@ __global__ __launch_bounds__(WAVE_ROW ? 64 * kNRows : 1024) void norm_kernel(con
             const int h = (c * threads + tid) * 8;
             float w[8];
             if (a.post_w != nullptr) {
-                load8_param<VEC>(a.post_w, 0, a.p_type, h, H, w);
+                load8_param(a.post_w, 0, a.p_type, h, H, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     v[c][i] *= w[i] + a.w_offset;
             }
             if (a.gate != nullptr && a.gate_cs != 0) {
-                load8_param<VEC>(a.gate, t * a.gate_rs, a.p_type, h, H, w);
+                load8_param(a.gate, t * a.gate_rs, a.p_type, h, H, w);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     v[c][i] *= w[i];
@@ -194,7 +196,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 64 * kNRows : 1024) void norm_kernel(con
     if (a.r_out != nullptr) {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            store8<VEC>((RT*)a.r_out + t * a.ldr_out, (c * threads + tid) * 8, H, v[c]);
+            store8((RT*)a.r_out + t * a.ldr_out, (c * threads + tid) * 8, H, v[c]);
     }
     if (a.pre_w == nullptr)
         return;
@@ -209,12 +211,12 @@ __global__ __launch_bounds__(WAVE_ROW ? 64 * kNRows : 1024) void norm_kernel(con
     for (int c = 0; c < NC; ++c) {
         const int h = (c * threads + tid) * 8;
         float w[8];
-        load8_param<VEC>(a.pre_w, 0, a.p_type, h, H, w);
+        load8_param(a.pre_w, 0, a.p_type, h, H, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[c][i] *= mul * (w[i] + a.w_offset);
         if (a.y != nullptr)
-            store8<VEC>(a.y + t * a.ldy, h, H, v[c]);
+            store8(a.y + t * a.ldy, h, H, v[c]);
         if (a.q != nullptr) {
             // H is a multiple of 128: the 16 lanes of a block are all inside
             // the row or all behind it
@@ -243,13 +245,13 @@ __global__ __launch_bounds__(WAVE_ROW ? 64 * kNRows : 1024) void norm_kernel(con
 
 namespace {
 
-template <typename XT, typename RT, bool VEC>
+template <typename XT, typename RT>
 void launch_typed(const NormArgs& a, hipStream_t s)
 {
     const int chunks = (a.H + 7) / 8;
     const unsigned T = (unsigned)a.T;
     if (a.H <= kNormShortH) {
-        hipLaunchKernelGGL((norm_kernel<XT, RT, 1, true, VEC>), dim3((T + kNRows - 1) / kNRows),
+        hipLaunchKernelGGL((norm_kernel<XT, RT, 1, true>), dim3((T + kNRows - 1) / kNRows),
                            dim3(64 * kNRows), 0, s, a);
         return;
     }
@@ -259,20 +261,11 @@ void launch_typed(const NormArgs& a, hipStream_t s)
     const int nc = chunks <= 1024 ? (a.T > 512 ? 2 : 1) : chunks <= 2048 ? 2 : 4;
     const dim3 block((unsigned)(((chunks + nc - 1) / nc + 63) / 64 * 64));
     if (nc == 1)
-        hipLaunchKernelGGL((norm_kernel<XT, RT, 1, false, VEC>), dim3(T), block, 0, s, a);
+        hipLaunchKernelGGL((norm_kernel<XT, RT, 1, false>), dim3(T), block, 0, s, a);
     else if (nc == 2)
-        hipLaunchKernelGGL((norm_kernel<XT, RT, 2, false, VEC>), dim3(T), block, 0, s, a);
+        hipLaunchKernelGGL((norm_kernel<XT, RT, 2, false>), dim3(T), block, 0, s, a);
     else
-        hipLaunchKernelGGL((norm_kernel<XT, RT, 4, false, VEC>), dim3(T), block, 0, s, a);
-}
-
-template <typename XT, typename RT>
-void launch_aligned(const NormArgs& a, hipStream_t s)
-{
-    if (a.aligned)
-        launch_typed<XT, RT, true>(a, s);
-    else
-        launch_typed<XT, RT, false>(a, s);
+        hipLaunchKernelGGL((norm_kernel<XT, RT, 4, false>), dim3(T), block, 0, s, a);
 }
 
 }  // namespace
@@ -281,9 +274,9 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s)
 {
     const bool x32 = a.x_type == W4A8_TYPE_FP32, r32 = a.r_type == W4A8_TYPE_FP32;
     if (x32)
-        r32 ? launch_aligned<float, float>(a, s) : launch_aligned<float, uint16_t>(a, s);
+        r32 ? launch_typed<float, float>(a, s) : launch_typed<float, uint16_t>(a, s);
     else
-        r32 ? launch_aligned<uint16_t, float>(a, s) : launch_aligned<uint16_t, uint16_t>(a, s);
+        r32 ? launch_typed<uint16_t, float>(a, s) : launch_typed<uint16_t, uint16_t>(a, s);
     return hipGetLastError();
 }
 
