@@ -176,8 +176,6 @@ int w4a8_gemm_epilogue(const uint8_t* a_e4m3, const float* a_scales, int64_t M, 
     d.ldr = ld_residual;
     d.out = (uint16_t*)out_bf16;
     d.ldo = ld_out;
-    d.vec4 = N % 4 == 0 && ld_out % 4 == 0 && (residual_bf16 == nullptr || ld_residual % 4 == 0);
-    d.vec2 = N % 2 == 0 && ld_out % 2 == 0 && (residual_bf16 == nullptr || ld_residual % 2 == 0);
     return hip_status(w4a8::launch_dense_epilogue(d, workspace, stream));
 }
 

@@ -260,9 +260,6 @@ struct DenseArgs {
     int64_t ldr;
     uint16_t* out;
     int64_t ldo;
-    // four (two) columns of a row are 8-byte (4-byte) aligned in out and
-    // residual, and N is a multiple of them
-    int vec4, vec2;
 };
 size_t dense_epilogue_workspace(int64_t M, int64_t K, int64_t N, int act);
 bool dense_epilogue_fits(int64_t M, int64_t K, int64_t N, int act);
