@@ -468,7 +468,7 @@ int w4a8_fused_moe_prepacked_noalloc(const void* hidden_bf16, int64_t T, int64_t
  * E/num_groups, 1 <= topk_groups <= num_groups, num_groups divides E
  * (INVALID_ARG otherwise); E <= 1024, T <= 2^25, num_groups <= 64, num_tokens
  * 4-byte aligned, pointers 16-byte aligned (UNSUPPORTED otherwise).  Any row
- * stride; rows of 16-byte aligned start and length are read with wide loads.
+ * stride.
  */
 #define W4A8_SCORE_SIGMOID 0
 #define W4A8_SCORE_SOFTMAX 1

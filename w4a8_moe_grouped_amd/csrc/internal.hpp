@@ -210,10 +210,9 @@ struct RouteArgs {
     const float* bias;  // [E] or null
     int softmax;        // score: softmax, else sigmoid
     int32_t groups, kept, group_top;
-    // set by the launcher: rows allow wide loads; with 16 lanes per token, lanes
-    // per group (a power of two), experts per lane, and whether every lane's
-    // are whole
-    int wide, run_log2, per, whole;
+    // set by the launcher, for 16 lanes per token: lanes per group (a power of
+    // two) and experts per lane
+    int run_log2, per;
     int32_t topk;
     int renorm;
     float scale;

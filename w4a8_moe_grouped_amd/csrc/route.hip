@@ -188,34 +188,52 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t i)
     return a.type == W4A8_TYPE_BF16 ? __uint_as_float(h << 16) : half_bits(h);
 }
 
-// logits e0 .. e0 + count - 1 of a row, then -inf.  a.wide: every row starts at
-// a multiple of 16 bytes, e0 is one of PL, and a lane has PL experts or none.
+// wide accesses at the alignment of an element, which are one instruction also
+// where they are misaligned (32768 x 256 in rows of 257: 18 us, element by
+// element 26; 32768 x 250 of bf16: 11.4 and 21)
+typedef float float4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef float float2_any __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t uint4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t uint2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t uint1_any __attribute__((aligned(2)));
+
+// logits e0 .. e0 + count - 1 of a row, then -inf; a lane whose PL logits all lie
+// in the row reads them at once, whose ever they are (E: the row's length)
 template <int PL>
 __device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0, int count, float* x)
 {
+    const bool inside = count > 0 && e0 + PL <= a.E;
+    auto cut = [&] {
+        if (count < PL) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                x[i] = i < count ? x[i] : -__builtin_inff();
+        }
+    };
 #pragma unroll
     for (int i = 0; i < PL; ++i)
         x[i] = -__builtin_inff();
     if (a.type == W4A8_TYPE_FP32) {
         const float* p = (const float*)a.logits + row + e0;
-        if (!a.wide) {
+        if (!inside) {
 #pragma unroll
             for (int i = 0; i < PL; ++i)
                 if (i < count)
                     x[i] = p[i];
-        } else if (count > 0) {
+        } else {
             if constexpr (PL >= 4) {
 #pragma unroll
                 for (int i = 0; i < PL; i += 4) {
-                    const float4 v = *(const float4*)(p + i);
+                    const float4_any v = *(const float4_any*)(p + i);
                     x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
                 }
             } else if constexpr (PL == 2) {
-                const float2 v = *(const float2*)p;
+                const float2_any v = *(const float2_any*)p;
                 x[0] = v.x, x[1] = v.y;
             } else {
                 x[0] = *p;
             }
+            cut();
         }
         return;
     }
@@ -226,24 +244,24 @@ __device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0
     for (int i = 0; i < (PL + 1) / 2; ++i)
         raw[i] = none | none << 16;
     const uint16_t* p = (const uint16_t*)a.logits + row + e0;
-    if (!a.wide) {
+    if (!inside) {
 #pragma unroll
         for (int i = 0; i < PL; ++i)
             if (i < count)
                 raw[i / 2] = (i & 1) ? (raw[i / 2] & 0xFFFFu) | (uint32_t)p[i] << 16
                                      : (raw[i / 2] & 0xFFFF0000u) | p[i];
-    } else if (count > 0) {
+    } else {
         if constexpr (PL >= 8) {
 #pragma unroll
             for (int i = 0; i < PL / 8; ++i) {
-                const uint4 v = *(const uint4*)(p + 8 * i);
+                const uint4_any v = *(const uint4_any*)(p + 8 * i);
                 raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
             }
         } else if constexpr (PL == 4) {
-            const uint2 v = *(const uint2*)p;
+            const uint2_any v = *(const uint2_any*)p;
             raw[0] = v.x, raw[1] = v.y;
         } else if constexpr (PL == 2) {
-            raw[0] = *(const uint32_t*)p;
+            raw[0] = *(const uint1_any*)p;
         } else {
             raw[0] = *p;
         }
@@ -257,6 +275,7 @@ __device__ __forceinline__ void load_run(const RouteArgs& a, int64_t row, int e0
         for (int i = 0; i < PL; ++i)
             x[i] = half_bits((i & 1) ? raw[i / 2] >> 16 : raw[i / 2] & 0xFFFFu);
     }
+    cut();
 }
 
 }  // namespace
@@ -650,13 +669,11 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
 #pragma unroll
             for (int i = 0; i < PL; ++i)
                 b[i] = 0.0f;
-            if (a.whole) {
-                if (count > 0) {
+            if (count > 0 && e0 + PL <= a.E) {
 #pragma unroll
-                    for (int i = 0; i < PL; i += 4) {
-                        const float4 v = *(const float4*)(a.bias + e0 + i);
-                        b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
-                    }
+                for (int i = 0; i < PL; i += 4) {
+                    const float4_any v = *(const float4_any*)(a.bias + e0 + i);
+                    b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
                 }
             } else {
 #pragma unroll
@@ -800,13 +817,10 @@ template <int PL>
 void launch_lanes(const RouteArgs& a, bool scores, hipStream_t s)
 {
     const dim3 grid((unsigned)((a.T + kRWaves - 1) / kRWaves)), block(64 * kRWaves);
-    RouteArgs b = a;
-    const int elem = a.type == W4A8_TYPE_FP32 ? 4 : 2;
-    b.wide = (a.ld * elem) % 16 == 0 && a.E % PL == 0;
     if (scores)
-        hipLaunchKernelGGL((route_kernel<PL, true>), grid, block, 0, s, b);
+        hipLaunchKernelGGL((route_kernel<PL, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((route_kernel<PL, false>), grid, block, 0, s, b);
+        hipLaunchKernelGGL((route_kernel<PL, false>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -834,11 +848,8 @@ bool try_rows(RouteArgs a, int per, int run_log2, hipStream_t s)
 {
     if (per > PL)
         return false;
-    const int size = a.E / a.groups;
     a.per = a.groups == 1 ? PL : per;
     a.run_log2 = run_log2;
-    a.whole = a.per == PL && size % PL == 0;
-    a.wide = a.whole && (a.ld * (a.type == W4A8_TYPE_FP32 ? 4 : 2)) % 16 == 0;
     if (a.topk <= 8)
         launch_rows<PL, 8>(a, s);
     else
