@@ -125,6 +125,26 @@ def test_route_near_ties(dev, dtype, E, groups, kept):
                 check_route(x, 8, score=score, bias=bias, num_groups=groups, topk_groups=kept, group_top=top)
 
 
+@pytest.mark.parametrize("dtype", [FP32, BF16, FP16])
+@pytest.mark.parametrize("T, E, k, groups, kept", [
+    (37, 512, 8, 1, 1), (37, 257, 16, 1, 1), (5, 440, 8, 8, 4), (70, 512, 8, 16, 3), (9, 444, 7, 2, 2), (3, 384, 12, 6, 2)])
+def test_route_with_32_experts_a_lane(dev, dtype, T, E, k, groups, kept):
+    """Random logits, logits a few steps apart, strides, specials."""
+    g = gen(dev, T + E)
+    x = padded(torch.randn(T, E, generator=g, device=dev).to(dtype), 3)
+    x[0] = -INF
+    x[1, ::2] = math.nan
+    x[2, 5:] = -INF
+    near = (1 + torch.finfo(dtype).eps * torch.randint(0, 9, (30, E), generator=g, device=dev)).to(dtype)
+    bias = 0.2 * torch.randn(E, generator=g, device=dev)
+    for score in ("sigmoid", "softmax"):
+        for b in (None, bias, torch.zeros(E, device=dev)):
+            for renorm, top in ((True, 2), (False, 1)):
+                for rows in (x, near):
+                    check_route(rows, k, score=score, bias=b, num_groups=groups, topk_groups=kept, group_top=top,
+                                renormalize=renorm)
+
+
 def test_route_orders_scores_that_32_bits_round_alike(dev):
     """sigmoid(x) + b around 1e-4 with a bias of 1000: 32 bits see ties."""
     E = 128

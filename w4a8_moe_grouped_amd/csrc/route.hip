@@ -590,7 +590,8 @@ enum RowKey { KEY_CHOICE, KEY_LOGIT32, KEY_LOGIT16 };
 template <int PL, int KEY, int KM>  // KM: most experts per token, 8 or 16
 __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
 {
-    constexpr uint32_t kSlots = 15;  // low bits of a key: 15 - slot
+    constexpr uint32_t kSlots = PL <= 16 ? 15 : 31;       // low bits of a key: kSlots - slot
+    constexpr uint32_t kIndexes = PL <= 16 ? 0xFF : 0x1FF;  // of KEY_LOGIT16: kIndexes - index
     const float ninf = -__builtin_inff();
     const int lane = threadIdx.x & 63, l = lane & 15;
     const int waves = (int)blockDim.x >> 6;
@@ -640,8 +641,8 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     }
     // choices in fp32, off by at most `off` + 2^-23 of their value: the
     // sigmoid's product, exp2, sum and reciprocal cost 2^-22 (kept: 2^-21), the
-    // softmax's sum of up to 20 roundings 2^-19.7 of its terms, the largest of
-    // which is 1 / sum (kept: 2^-19 of that)
+    // softmax's sum of up to 20 (PL 32: 36) roundings 2^-19.7 (2^-18.8) of its
+    // terms, the largest of which is 1 / sum (kept: 2^-19, 2^-18 of that)
     const bool sums = a.groups > 1 && a.group_top == 2;
     float off = 0x1p-21f;
     uint32_t key[PL], gkey[PL];  // of the experts' order, and of the groups'
@@ -655,7 +656,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
                 sum += c[i];
             }
             const float inv = __builtin_amdgcn_rcpf(row_sum16(sum));
-            off = 0x1p-19f * inv;
+            off = (PL <= 16 ? 0x1p-19f : 0x1p-18f) * inv;
 #pragma unroll
             for (int i = 0; i < PL; ++i)
                 c[i] *= inv;
@@ -734,7 +735,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     }
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-        key[i] = KEY == KEY_LOGIT16 ? (key[i] & ~0xFFu) | (uint32_t)(0xFF - e0 - i)
+        key[i] = KEY == KEY_LOGIT16 ? (key[i] & ~kIndexes) | (uint32_t)((int)kIndexes - e0 - i)
                                     : (key[i] & ~kSlots) | (uint32_t)(kSlots - i);
     sort_down(key);
     key[0] = open ? key[0] : 0;  // this lane never holds the largest
@@ -747,9 +748,9 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     bool near = false;  // too close to the next one for the keys to tell
     if (KEY != KEY_LOGIT16 && chosen && next > kNoKey) {
         if (KEY == KEY_CHOICE) {
-            // both off by `off` + 2^-23 and 15 steps of 2^-23 for the slot
+            // both off by `off` + 2^-23 and 15 (31) steps of 2^-23 for the slot
             const float v = key_value(mine), w = key_value(next);
-            near = !(v - w > 2.0f * off + 0x1p-18f * (fabsf(v) + fabsf(w)));
+            near = !(v - w > 2.0f * off + (PL <= 16 ? 0x1p-18f : 0x1p-17f) * (fabsf(v) + fabsf(w)));
         } else {
             near = ((mine ^ next) & ~kSlots) == 0;
         }
@@ -758,7 +759,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     double s = 0.0, exact = kNone;
     if (chosen) {
         const uint32_t lanes = ((lane & 32 ? lanes_hi : lanes_lo) >> (lane & 16)) & 0xFFFF;
-        my_id = KEY == KEY_LOGIT16 ? (int)(0xFF - (mine & 0xFF))
+        my_id = KEY == KEY_LOGIT16 ? (int)(kIndexes - (mine & kIndexes))
                                    : first_of(__ffs((int)lanes) - 1) + (int)(kSlots - (mine & kSlots));
         close |= KEY != KEY_LOGIT16 && (lanes & (lanes - 1)) != 0;  // one key in several lanes: all gave it up
         const float v = load_logit(a, row + my_id);
@@ -806,7 +807,7 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
                 else if (PL == 8)
                     route_token<2, true>(a, t0 + r);
                 else
-                    route_token<4, true>(a, t0 + r);
+                    route_token<PL / 4, true>(a, t0 + r);
             }
     }
 }
@@ -842,7 +843,7 @@ void launch_rows(const RouteArgs& a, hipStream_t s)
 }
 
 // rows of 16 lanes: up to 16 experts of at most 16 groups, each of which gets
-// the lanes of a power of two and fits them with 16 experts a lane
+// the lanes of a power of two and fits them with 32 experts a lane
 template <int PL>
 bool try_rows(RouteArgs a, int per, int run_log2, hipStream_t s)
 {
@@ -860,7 +861,8 @@ bool try_rows(RouteArgs a, int per, int run_log2, hipStream_t s)
 }  // namespace
 
 // Four tokens per wave where their rows fit 16 lanes, else one (32768 tokens,
-// 256 experts in 8 groups, top 8: 20 us against 52).
+// 256 experts in 8 groups, top 8: 20 us against 52; 8192 tokens, 440 experts,
+// top 8: 17 us against 27).
 hipError_t launch_route(const RouteArgs& a, hipStream_t s)
 {
     if (a.topk <= 16 && a.groups <= 16) {
@@ -868,7 +870,8 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s)
         while ((16 >> run_log2) < a.groups)
             --run_log2;
         const int lanes = 1 << run_log2, per = (a.E / a.groups + lanes - 1) / lanes;
-        if (try_rows<4>(a, per, run_log2, s) || try_rows<8>(a, per, run_log2, s) || try_rows<16>(a, per, run_log2, s))
+        if (try_rows<4>(a, per, run_log2, s) || try_rows<8>(a, per, run_log2, s) || try_rows<16>(a, per, run_log2, s) ||
+            try_rows<32>(a, per, run_log2, s))
             return hipGetLastError();
     }
     const bool scores =
