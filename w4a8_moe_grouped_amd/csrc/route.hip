@@ -483,8 +483,11 @@ __global__ __launch_bounds__(64 * kRWaves) void route_kernel(const RouteArgs a)
 // sorts its own with a plain min/max network, and a round is a DPP maximum
 // over the row of 16 lanes that leaves the result in all of them; scores are
 // fp32.  That decides every token whose neighbouring choices differ by more
-// than both can be off; the others (about one in 500 of N(0,1) logits with a
-// bias) are done again by route_token, the whole wave on one token.
+// than both can be off.  Closer ones are put in order by their 64-bit values,
+// which the weights need anyway; where even these leave open which experts are
+// chosen, or a group's place is too close to tell, route_token does the token
+// again, the whole wave on it (8192 tokens, 440 experts, a bias: 12 us; with
+// every disorder done again 18).
 
 namespace {
 
@@ -540,10 +543,15 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N])
                     }
 }
 
+// What orders the experts: their choice in fp32 (with a bias), or their logits
+// (without), exactly for the 16-bit types, whose keys hold the index too (they
+// leave the low 13 or 16 bits of a float free).
+enum RowKey { KEY_CHOICE, KEY_LOGIT32, KEY_LOGIT16 };
+
 // Rounds J .. topk - 1 of the search, unrolled (a loop left rolled indexes the
 // keys at run time: 2.5 us a round): lane J of each row gets the row's largest
-// key and the lanes that held it, and these move on to their next.
-template <int J, int KM, int PL>
+// key and the lane that held it, and this moves on to its next.
+template <int J, int KM, int KEY, int PL>
 __device__ __forceinline__ void take_best(uint32_t (&key)[PL], int topk, int l, uint32_t& mine, uint32_t& lanes_lo,
                                           uint32_t& lanes_hi)
 {
@@ -551,16 +559,34 @@ __device__ __forceinline__ void take_best(uint32_t (&key)[PL], int topk, int l, 
         if (J == topk)
             return;
         const uint32_t m = row_max(key[0]);
-        const bool won = key[0] == m;
-        const uint64_t lanes = __ballot(won);
+        bool won = key[0] == m;
+        uint64_t lanes = __ballot(won);
+        // every row has a winner, so no difference borrows from its neighbour
+        if (KEY != KEY_LOGIT16 && (lanes & (lanes - 0x0001000100010001ull)) != 0) {  // one key in several lanes
+            won = won && ((lanes >> (threadIdx.x & 48)) & ((1u << l) - 1)) == 0;     // the lowest first
+            lanes = __ballot(won);
+        }
         mine = l == J ? m : mine;
         lanes_lo = l == J ? (uint32_t)lanes : lanes_lo;
         lanes_hi = l == J ? (uint32_t)(lanes >> 32) : lanes_hi;
-        // as far as later rounds can ask for them
+        // as far as later rounds, and the one behind them, can ask for them
 #pragma unroll
-        for (int i = 0; i < KM - J && i < PL; ++i)
+        for (int i = 0; i <= KM - J && i < PL; ++i)
             key[i] = won ? (i + 1 < PL ? key[i + 1] : 0) : key[i];
-        take_best<J + 1, KM>(key, topk, l, mine, lanes_lo, lanes_hi);
+        take_best<J + 1, KM, KEY>(key, topk, l, mine, lanes_lo, lanes_hi);
+    }
+}
+
+// how many lanes of the row come before this one by value, then index
+template <int N>
+__device__ __forceinline__ int count_ahead(double value, int id)
+{
+    if constexpr (N < 16) {
+        const double v = dpp_d<kRor + N>(value);
+        const int i = (int)dpp_u<kRor + N>((uint32_t)id);
+        return ((v > value || (v == value && i < id)) ? 1 : 0) + count_ahead<N + 1>(value, id);
+    } else {
+        return 0;
     }
 }
 
@@ -581,11 +607,6 @@ __device__ __forceinline__ void rank_groups(float mine, int l, int run, float sl
 }
 
 }  // namespace
-
-// What orders the experts: their choice in fp32 (with a bias), or their logits
-// (without), exactly for the 16-bit types, whose keys hold the index too (they
-// leave the low 13 or 16 bits of a float free).
-enum RowKey { KEY_CHOICE, KEY_LOGIT32, KEY_LOGIT16 };
 
 template <int PL, int KEY, int KM>  // KM: most experts per token, 8 or 16
 __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
@@ -739,36 +760,51 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
                                     : (key[i] & ~kSlots) | (uint32_t)(kSlots - i);
     sort_down(key);
     key[0] = open ? key[0] : 0;  // this lane never holds the largest
-    uint32_t mine = 0, lanes_lo = 0, lanes_hi = 0;  // lane j: key j, and which lanes held it
-    take_best<0, KM>(key, a.topk, l, mine, lanes_lo, lanes_hi);
+    uint32_t mine = 0, lanes_lo = 0, lanes_hi = 0;  // lane j: key j, and which lane held it
+    take_best<0, KM, KEY>(key, a.topk, l, mine, lanes_lo, lanes_hi);
     const uint32_t rest = row_max(key[0]);  // the best that is not chosen
     const uint32_t after = dpp_u<0x101>(mine);  // row_shl: of lane l + 1
     const uint32_t next = l + 1 == a.topk ? rest : after;
     const bool chosen = l < a.topk && mine > kNoKey;
-    bool near = false;  // too close to the next one for the keys to tell
-    if (KEY != KEY_LOGIT16 && chosen && next > kNoKey) {
-        if (KEY == KEY_CHOICE) {
-            // both off by `off` + 2^-23 and 15 (31) steps of 2^-23 for the slot
-            const float v = key_value(mine), w = key_value(next);
-            near = !(v - w > 2.0f * off + (PL <= 16 ? 0x1p-18f : 0x1p-17f) * (fabsf(v) + fabsf(w)));
-        } else {
-            near = ((mine ^ next) & ~kSlots) == 0;
-        }
-    }
+    // whether a chosen key and a lower one are too close to tell
+    auto too_near = [&](uint32_t high, uint32_t low) {
+        if (KEY == KEY_LOGIT16 || low <= kNoKey)
+            return false;
+        if (KEY == KEY_LOGIT32)
+            return ((high ^ low) & ~kSlots) == 0;
+        // both off by `off` + 2^-23 and 15 (31) steps of 2^-23 for the slot
+        const float v = key_value(high), w = key_value(low);
+        return !(v - w > 2.0f * off + (PL <= 16 ? 0x1p-18f : 0x1p-17f) * (fabsf(v) + fabsf(w)));
+    };
+    const bool near = chosen && too_near(mine, next);
     int my_id = -1;
+    int place = l;
     double s = 0.0, exact = kNone;
     if (chosen) {
         const uint32_t lanes = ((lane & 32 ? lanes_hi : lanes_lo) >> (lane & 16)) & 0xFFFF;
         my_id = KEY == KEY_LOGIT16 ? (int)(kIndexes - (mine & kIndexes))
                                    : first_of(__ffs((int)lanes) - 1) + (int)(kSlots - (mine & kSlots));
-        close |= KEY != KEY_LOGIT16 && (lanes & (lanes - 1)) != 0;  // one key in several lanes: all gave it up
         const float v = load_logit(a, row + my_id);
         s = a.softmax ? exp_below64(v, top) : sigmoid64(v);
         exact = (double)v;
     }
     if (KEY != KEY_LOGIT16 && __ballot(near) != 0) {
-        // two chosen ones that 64 bits find in order are fine; the last chosen
-        // one against all the others is not known that way
+        // The chosen ones are ordered by their 64-bit values.  They are the
+        // right ones if the best that is not chosen is below all of them, in
+        // 64 bits where it is near the last, and the one behind that far
+        // enough (one key in several lanes: more than one is as good).
+        const bool best = key[0] == rest && rest > kNoKey;
+        const uint64_t all = __ballot(best);
+        const uint32_t holders = ((uint32_t)(lane & 32 ? all >> 32 : all) >> (lane & 16)) & 0xFFFF;
+        const uint32_t behind = row_max(best ? key[1] : key[0]);
+        const bool last = near && l + 1 == a.topk;
+        const bool against = chosen && ((__ballot(last) >> (lane & 48)) & 0xFFFF) != 0;
+        int rest_id = 0;
+        double rest_value = kNone;
+        if (against) {
+            rest_id = first_of(__ffs((int)holders) - 1) + (int)(kSlots - (rest & kSlots));
+            rest_value = (double)load_logit(a, row + rest_id);
+        }
         if (KEY == KEY_CHOICE) {
             double whole = total;
             if (a.softmax && a.renorm) {  // not needed so far, and seldom here
@@ -782,11 +818,15 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
             }
             if (chosen)
                 exact = (a.softmax ? s / whole : s) + (double)a.bias[my_id];
+            if (against) {
+                const float v = (float)rest_value;
+                rest_value = (a.softmax ? exp_below64(v, top) / whole : sigmoid64(v)) + (double)a.bias[rest_id];
+            }
         }
-        const double other = dpp_d<0x101>(exact);
-        const int other_id = (int)dpp_u<0x101>((uint32_t)my_id);
-        const bool ordered = l + 1 < a.topk && (exact > other || (exact == other && my_id < other_id));
-        close |= near && !ordered;
+        close |= chosen && !(exact > rest_value || (exact == rest_value && my_id < rest_id));  // NaN: close
+        close |= last && ((holders & (holders - 1)) != 0 || too_near(mine, behind));
+        const int ahead = count_ahead<1>(exact, my_id);
+        place = chosen ? ahead : l;
     }
     if (a.renorm) {
         const double sum = run_sum<0>(s, a.topk);
@@ -796,8 +836,8 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
     }
     const uint64_t again = KEY != KEY_LOGIT16 || sums ? __ballot(close && live) : 0;
     if (t < a.T && l < a.topk && ((again >> (lane & 48)) & 0xFFFF) == 0) {
-        a.ids[t * a.topk + l] = my_id;
-        a.weights[t * a.topk + l] = (float)((double)a.scale * s);
+        a.ids[t * a.topk + place] = my_id;
+        a.weights[t * a.topk + place] = (float)((double)a.scale * s);
     }
     if (again != 0) {
         for (int r = 0; r < 4; ++r)
@@ -862,7 +902,7 @@ bool try_rows(RouteArgs a, int per, int run_log2, hipStream_t s)
 
 // Four tokens per wave where their rows fit 16 lanes, else one (32768 tokens,
 // 256 experts in 8 groups, top 8: 20 us against 52; 8192 tokens, 440 experts,
-// top 8: 17 us against 27).
+// top 8: 12 us against 27).
 hipError_t launch_route(const RouteArgs& a, hipStream_t s)
 {
     if (a.topk <= 16 && a.groups <= 16) {
