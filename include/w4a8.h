@@ -497,7 +497,8 @@ int w4a8_moe_route(const void* logits, int logits_type, int64_t T, int64_t E, in
  *                gate_col_stride]: row stride 0 for one gate for all tokens,
  *                column stride 1, or 0 for one value per token
  *   residual_out [T, H] of residual_type, row stride ldr_out, or NULL: r'.
- *                It may be `residual` itself (same stride)
+ *                It may be `residual` itself (same stride); no other output
+ *                overlaps an operand or another output
  *   y_bf16       [T, H] bf16, row stride ldy, or NULL
  *   q_e4m3       [T, H] e4m3 codes of y, row stride H, with
  *   q_scales     [T, H/128] fp32, by the rule of w4a8_quantize_act on the
@@ -529,9 +530,11 @@ int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* resid
  *                (exact and tanh form), and SwiGLU
  *   residual     [M, N] bf16, row stride ld_residual >= N, or NULL; it may be
  *                out itself (same stride)
- *   out_bf16     [M, N], row stride ld_out >= N
+ *   out_bf16     [M, N], row stride ld_out >= N; overlaps no other operand
  *   workspace    device scratch of *workspace_bytes bytes (query with NULL; it
- *                depends on M, K, N and activation alone, and may be 0)
+ *                depends on M, K, N and activation alone, and may be 0).  Calls
+ *                that may run at once, replays of captured graphs among them,
+ *                need one each
  * M >= 0 (M == 0 launches nothing), N > 0, K > 0 (INVALID_ARG otherwise), K %
  * 128 == 0, K <= 2^22, M, R < 2^31, launches below 2^32 threads (met by up to
  * 2^33 outputs with M % 32 == 0 and 2^36 weights), pointers 16-byte aligned
