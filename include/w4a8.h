@@ -48,7 +48,9 @@
  *  - Workspace: pass workspace == NULL to query; the required size (a pure
  *    function of the shape arguments) is written to *workspace_bytes and
  *    W4A8_OK is returned.  Otherwise *workspace_bytes must hold the size of
- *    the buffer supplied.
+ *    the buffer supplied.  A call computes only with a non-null workspace,
+ *    also where the required size is 0: any 16-byte aligned address then
+ *    does, it is not followed.
  *  - Calls that share a workspace or outputs must be ordered by the caller.
  *  - Size limits (W4A8_ERR_UNSUPPORTED beyond them): the kernels address each
  *    operand through a buffer resource with 32-bit extent and offsets, so the

@@ -168,3 +168,11 @@ def test_ref_gemm_is_the_oracle(orc):
 def test_gemm_epilogue_threads_of_one_launch(L, M, K, N, act, want):
     """Both kernels' launches hold less than 2^32 threads; the query says so."""
     assert _gemm(L, M=M, K=K, N=N, act=act, ldo=N, ws=None) == want
+
+
+def test_gemm_epilogue_without_workspace_bytes(L):
+    """0 bytes are enough where the query says so, at an address that is not null."""
+    assert w4.gemm_epilogue_workspace_bytes(64, 2048, 7168) == 0
+    assert _gemm(L, K=2048, N=7168, ldo=7168, nbytes=0) == OK
+    assert _gemm(L, M=4, a=None, nbytes=0) == INVALID  # not taken for a query
+    assert _gemm(L, M=4, a=None, ws=None, nbytes=0) == OK

@@ -722,3 +722,29 @@ def test_binding_checks_on_the_gpu(dev):
             w4.gemm_epilogue(*ops, **bad)
     with pytest.raises(w4.W4A8Error):
         w4.gemm_epilogue(ops[0], ops[1], ops[2][:31], ops[3][:31], activation="swiglu")
+
+
+@pytest.mark.parametrize("M", [1, 64, 333])
+def test_gemm_epilogue_with_an_empty_workspace(dev, M):
+    """Sizes that need no workspace take an empty one, whose address is null."""
+    K, N = 1664, 130
+    ops = gemm_inputs(dev, M, K, N)
+    assert w4.gemm_epilogue_workspace_bytes(M, K, N) == 0
+    whole = torch.zeros(64, dtype=torch.uint8, device=dev)
+    for ws in (torch.empty(0, dtype=torch.uint8, device=dev), whole[:0], whole):
+        out = torch.full((M, N), math.nan, dtype=BF16, device=dev)
+        assert w4.gemm_epilogue(*ops, out=out, workspace=ws) is out
+        check_gemm(ops, got=out)
+
+
+def test_gemm_epilogue_refuses_an_empty_workspace_for_tiles(dev):
+    ops = gemm_inputs(dev, 4096, 256, 4096)
+    need = w4.gemm_epilogue_workspace_bytes(4096, 256, 4096)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    for bad in (ws[:0], torch.empty(0, dtype=torch.uint8, device=dev), ws[:need - 1]):
+        with pytest.raises(w4.W4A8Error, match="workspace"):
+            w4.gemm_epilogue(*ops, workspace=bad)
+    for bad in (torch.empty(0, dtype=torch.uint8), torch.empty(need, dtype=torch.uint8)):  # in host memory
+        with pytest.raises(w4.W4A8Error, match="one GPU"):
+            w4.gemm_epilogue(*ops, workspace=bad)

@@ -38,6 +38,10 @@ StatusFn g_status = nullptr;
 constexpr int64_t kGroup = 128;
 constexpr int kActSwiglu = 5;
 
+// named by a call that needs no workspace, and never followed: null would ask
+// for the size, and null is the address of every empty tensor
+alignas(16) char g_no_workspace[16];
+
 // the message of a W4A8Error
 struct Refused : std::runtime_error {
     using std::runtime_error::runtime_error;
@@ -417,24 +421,26 @@ PyObject* gemm_epilogue(PyObject*, PyObject* const* a, Py_ssize_t n)
         const float *sap = (const float*)addr(&sa, device), *swp = (const float*)addr(&sw, device);
         const uint8_t *qp = (const uint8_t*)addr(&q, device), *wp = (const uint8_t*)addr(&w, device);
         if (M > 0) {
-            size_t bytes = 0;
-            if (ws == nullptr) {
-                launch("w4a8_gemm_epilogue(query)", [&] {
-                    return g_gemm(nullptr, nullptr, M, K, nullptr, nullptr, N, nullptr, 0, act, nullptr, N, nullptr, N,
-                                  nullptr, &bytes, nullptr);
-                });
-                if (bytes > 0)
-                    made_ws = make({(int64_t)bytes}, at::kByte, device), ws = &made_ws;
-            } else {
+            size_t need = 0;
+            launch("w4a8_gemm_epilogue(query)", [&] {
+                return g_gemm(nullptr, nullptr, M, K, nullptr, nullptr, N, nullptr, 0, act, nullptr, N, nullptr, N, nullptr,
+                              &need, nullptr);
+            });
+            if (ws != nullptr) {
+                addr(ws, device);
                 if (!ws->is_contiguous())
                     refuse("workspace must be contiguous");
-                bytes = ws->numel() * ws->element_size();
+                const size_t given = ws->numel() * ws->element_size();
+                if (given < need)
+                    refuse("workspace holds " + std::to_string(given) + " bytes, " + std::to_string(need) + " are needed");
+            } else if (need > 0) {
+                made_ws = make({(int64_t)need}, at::kByte, device), ws = &made_ws;
             }
-            // a call that needs none still names a buffer (null asks for the size)
-            void* wsp = ws != nullptr ? addr(ws, device) : op;
+            void* const given = addr(ws, device);
+            void* const wsp = need > 0 ? given : g_no_workspace;
             const Stream s = stream_of(device);
             launch("w4a8_gemm_epilogue", [&] {
-                return g_gemm(qp, sap, M, K, wp, swp, N, bp, bias_type, act, rp, ldr, op, ldo, wsp, &bytes, s);
+                return g_gemm(qp, sap, M, K, wp, swp, N, bp, bias_type, act, rp, ldr, op, ldo, wsp, &need, s);
             });
         }
         return given_or(a[7], made_out);

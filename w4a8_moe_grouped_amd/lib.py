@@ -532,7 +532,9 @@ def gemm_epilogue(a_q: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
     """w4a8_gemm_epilogue: bf16 [M, N] = act(A * W^T + bias) + residual.  a_q,
     a_scales, w, w_scales as for gemm; with activation "swiglu" w has 2N rows
     (gate rows, then up rows).  bias: fp32 or bf16, one value per weight row;
-    residual: bf16 [M, N], may be out itself."""
+    residual: bf16 [M, N], may be out itself.  workspace: a contiguous tensor
+    of at least gemm_epilogue_workspace_bytes bytes, an empty one where that
+    is 0; allocated if not given."""
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise W4A8Error("activation must be one of %s" % (tuple(ACTIVATIONS),))
