@@ -748,3 +748,23 @@ def test_gemm_epilogue_refuses_an_empty_workspace_for_tiles(dev):
     for bad in (torch.empty(0, dtype=torch.uint8), torch.empty(need, dtype=torch.uint8)):  # in host memory
         with pytest.raises(w4.W4A8Error, match="one GPU"):
             w4.gemm_epilogue(*ops, workspace=bad)
+
+
+def test_gemm_with_an_empty_workspace(dev):
+    """gemm and the fused forward, too: computed where none is needed, else
+    refused."""
+    for M, K, N in ((1, 1024, 64), (48, 1024, 128), (700, 1024, 64)):
+        ops = gemm_inputs(dev, M, K, N)
+        out = torch.full((M, N), math.nan, dtype=BF16, device=dev)
+        empty = torch.empty(0, dtype=torch.uint8, device=dev)
+        if w4.gemm_workspace_bytes(M, K, N) == 0:
+            assert torch.equal(w4.gemm(*ops, out=out, workspace=empty), w4.gemm(*ops))
+        else:
+            with pytest.raises(w4.W4A8Error, match="workspace"):
+                w4.gemm(*ops, out=out, workspace=empty)
+    b = Block(dev, 8)
+    x = torch.randn(8, 512, device=dev, generator=gen(dev, 3)).to(BF16)
+    ids = torch.zeros(8, b.cfg.topk, dtype=torch.int32, device=dev)
+    for packed in (None, b.packed):
+        with pytest.raises(w4.W4A8Error, match="workspace"):
+            w4.fused_moe(x, ids, ids.float(), 0, 8, *b.w, workspace=b.ws[:0], prepacked=packed)

@@ -119,6 +119,19 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# Named by a call whose workspace is empty: an empty tensor's address is null,
+# which would ask for the size.  Not followed: the size 0 is refused, or is
+# all the call needs.
+_no_workspace = ctypes.create_string_buffer(32)
+_NO_WORKSPACE = (ctypes.addressof(_no_workspace) + 15) // 16 * 16
+
+
+def _workspace(t: torch.Tensor, rows: int):
+    """The address of the workspace of a call over `rows` rows (without any,
+    nothing is computed, whatever the workspace)."""
+    return ctypes.c_void_p(t.data_ptr() or (_NO_WORKSPACE if rows > 0 else None))
+
+
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -244,7 +257,7 @@ def fused_moe_fp4(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights: to
     n = ctypes.c_size_t(workspace.numel())
     _check(load().w4a8_fused_moe_fp4_prepacked(
         _ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_weights), k, expert_begin, E, I,
-        _ptr(w13p), _ptr(s13p), _ptr(w2p), _ptr(s2p), _ptr(out), _ptr(workspace),
+        _ptr(w13p), _ptr(s13p), _ptr(w2p), _ptr(s2p), _ptr(out), _workspace(workspace, T),
         ctypes.byref(n), _stream(hidden.device)), "w4a8_fused_moe_fp4_prepacked")
     return out
 
@@ -322,7 +335,7 @@ def fused_moe_bounded(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights
     _check(load().w4a8_fused_moe_bounded(
         _ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_weights), k, expert_begin, E, I,
         int(weight_format), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), int(max_local_pairs),
-        _ptr(local_pairs), _ptr(out), _ptr(workspace), ctypes.byref(n), _stream(hidden.device)),
+        _ptr(local_pairs), _ptr(out), _workspace(workspace, T), ctypes.byref(n), _stream(hidden.device)),
         "w4a8_fused_moe_bounded")
     return out, local_pairs
 
@@ -362,7 +375,7 @@ def fused_moe_persistent(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weig
     n = ctypes.c_size_t(workspace.numel())
     _check(load().w4a8_fused_moe_persistent(
         _ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_weights), k, expert_begin, E, I,
-        int(weight_format), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(out), _ptr(workspace),
+        int(weight_format), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(out), _workspace(workspace, T),
         ctypes.byref(n), _stream(hidden.device)),
         "w4a8_fused_moe_persistent")
     return out
@@ -394,7 +407,7 @@ def fused_moe_recipe(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights:
     _check(load().w4a8_fused_moe_recipe(
         _ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_weights), k, expert_begin, E, I,
         int(weight_format), _ptr(w13p), _ptr(s13p), _ptr(w2p), _ptr(s2p), int(down_act_group),
-        _ptr(out), _ptr(workspace), ctypes.byref(n), _stream(hidden.device)), "w4a8_fused_moe_recipe")
+        _ptr(out), _workspace(workspace, T), ctypes.byref(n), _stream(hidden.device)), "w4a8_fused_moe_recipe")
     return out
 
 
@@ -427,7 +440,7 @@ def gemm(a_q: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: t
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=a_q.device)
     n = ctypes.c_size_t(workspace.numel())
     _check(load().w4a8_gemm(_ptr(a_q), _ptr(a_scales), M, K, _ptr(w), _ptr(w_scales), N,
-                            _ptr(out), _ptr(workspace), ctypes.byref(n), _stream(a_q.device)),
+                            _ptr(out), _workspace(workspace, M), ctypes.byref(n), _stream(a_q.device)),
            "w4a8_gemm")
     return out
 
@@ -676,13 +689,13 @@ def fused_moe(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.
             _check(load().w4a8_fused_moe_prepacked_static(
                 _ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_weights), k, expert_begin, E, I,
                 _ptr(ws[0]), _ptr(ws[1]), _ptr(ws[2]), _ptr(ws[3]), stat[0], stat[1], _ptr(out),
-                _ptr(workspace), ctypes.byref(n), _stream(hidden.device)), "w4a8_fused_moe_prepacked_static")
+                _workspace(workspace, T), ctypes.byref(n), _stream(hidden.device)), "w4a8_fused_moe_prepacked_static")
             return out
     else:
         assert a1_scale is None and a2_scale is None, "static scales need prepacked weights"
         fn, name = load().w4a8_fused_moe, "w4a8_fused_moe"
         ws = (w13, s13, w2, s2)
     _check(fn(_ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_weights), k, expert_begin, E, I,
-              _ptr(ws[0]), _ptr(ws[1]), _ptr(ws[2]), _ptr(ws[3]), _ptr(out), _ptr(workspace),
+              _ptr(ws[0]), _ptr(ws[1]), _ptr(ws[2]), _ptr(ws[3]), _ptr(out), _workspace(workspace, T),
               ctypes.byref(n), _stream(hidden.device)), name)
     return out
