@@ -768,3 +768,18 @@ def test_gemm_with_an_empty_workspace(dev):
     for packed in (None, b.packed):
         with pytest.raises(w4.W4A8Error, match="workspace"):
             w4.fused_moe(x, ids, ids.float(), 0, 8, *b.w, workspace=b.ws[:0], prepacked=packed)
+
+
+def test_gemm_refuses_a_workspace_with_holes(dev):
+    """An expanded tensor names more elements than it holds."""
+    ops = gemm_inputs(dev, 128, 7168, 512)
+    need = w4.gemm_workspace_bytes(128, 7168, 512)
+    assert need > 0
+    holes = torch.zeros(16, 1, dtype=torch.uint8, device=dev).expand(16, need)
+    with pytest.raises(w4.W4A8Error, match="contiguous"):
+        w4.gemm(*ops, workspace=holes)
+    b = Block(dev, 8)
+    x = torch.zeros(8, 512, dtype=BF16, device=dev)
+    ids = torch.zeros(8, b.cfg.topk, dtype=torch.int32, device=dev)
+    with pytest.raises(w4.W4A8Error, match="contiguous"):
+        w4.fused_moe(x, ids, ids.float(), 0, 8, *b.w, workspace=holes[:, :b.ws.numel()])

@@ -128,7 +128,10 @@ _NO_WORKSPACE = (ctypes.addressof(_no_workspace) + 15) // 16 * 16
 
 def _workspace(t: torch.Tensor, rows: int):
     """The address of the workspace of a call over `rows` rows (without any,
-    nothing is computed, whatever the workspace)."""
+    nothing is computed, whatever the workspace).  Its size is taken from its
+    elements, so it has to hold them all."""
+    if not t.is_contiguous():
+        raise W4A8Error("workspace must be contiguous")
     return ctypes.c_void_p(t.data_ptr() or (_NO_WORKSPACE if rows > 0 else None))
 
 
