@@ -783,3 +783,32 @@ def test_gemm_refuses_a_workspace_with_holes(dev):
     ids = torch.zeros(8, b.cfg.topk, dtype=torch.int32, device=dev)
     with pytest.raises(w4.W4A8Error, match="contiguous"):
         w4.fused_moe(x, ids, ids.float(), 0, 8, *b.w, workspace=holes[:, :b.ws.numel()])
+
+
+@pytest.mark.parametrize("M, K, N", [(1, 2048, 96), (40, 2048, 96), (300, 2048, 96), (600, 2048, 96), (2500, 1024, 900),
+                                     (4096, 256, 4096)])
+def test_gemm_epilogue_small_weights(dev, M, K, N):
+    """The bound counts the products themselves: weights of 0 give 0 whatever
+    the activations, weights of -1, 0 and 1 are as exact as larger ones, and a
+    large activation under a weight of 0 costs its neighbours nothing."""
+    q, s, w, sw = gemm_inputs(dev, M, K, N, dist="positive")
+    zero = torch.zeros_like(w)
+    check_gemm((q, s, zero, sw))
+    check_gemm((torch.full_like(q, 0x7E), s, zero, sw), bias=torch.ones(N, device=dev))
+    some = zero.clone()
+    some[::2] = w[::2]  # every other weight row
+    check_gemm((q, s, some, sw))
+    g = gen(dev, K + N)
+    unit = lambda: torch.randint(0, 3, w.shape, generator=g, device=dev, dtype=torch.uint8)  # noqa: E731
+    signs = torch.tensor([0, 1, 15], dtype=torch.uint8, device=dev)
+    check_gemm((q, s, signs[unit().long()] | signs[unit().long()] << 4, sw))
+    check_gemm((torch.full_like(q, 0x7E), s, signs[unit().long()] | signs[unit().long()] << 4, sw))
+    # +-448 under a weight of 0 in every group, codes of 2^-4 to 2^-2 elsewhere
+    small = (0x18 + torch.randint(0, 16, q.shape, generator=g, device=dev, dtype=torch.uint8)) \
+        | torch.randint(0, 2, q.shape, generator=g, device=dev, dtype=torch.uint8) << 7
+    small[:, 10::128] = 0x7E
+    small[:, 75::128] = 0xFE
+    clear = w.clone()
+    clear[:, 5::64] &= 0xF0   # k = 10 of 128
+    clear[:, 37::64] &= 0x0F  # k = 75
+    check_gemm((small, s, clear, sw))

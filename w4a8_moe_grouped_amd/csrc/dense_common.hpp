@@ -9,25 +9,23 @@
 
 namespace w4a8 {
 
-// four nibbles (one per byte, two's complement) -> e4m3 codes of v * 2^-9:
-// |v| <= 7 are the subnormal codes |v|, 8 is code 0x08
-__device__ __forceinline__ uint32_t nibbles_to_e4m3(uint32_t b)
-{
-    const uint32_t s = (b >> 3) & 0x01010101u;  // sign per byte
-    const uint32_t m = s * 0x0Fu;
-    return ((b ^ m) + s) | (s << 7);
-}
-
-// 16 packed bytes (32 nibbles, k even in the low nibble) -> 32 e4m3 codes in
-// natural K order
+// 16 packed bytes (32 nibbles, two's complement, k even in the low one) -> 32
+// e4m3 codes of v * 2^-9 in natural K order: |v| <= 7 are the subnormal codes
+// |v|, 8 is code 0x08, the sign is bit 7.  Magnitudes are found in eight nibbles
+// at once ((7 ^ k) + 1 <= 8 leaves its nibble alone): 11 operations per 8 weights,
+// byte by byte 17.
 __device__ __forceinline__ v8i int4_to_fp8(const v4i& w)
 {
+    constexpr uint32_t kLow = 0x0F0F0F0Fu;
     v8i r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t x = (uint32_t)w[i];
-        const uint32_t lo = nibbles_to_e4m3(x & 0x0F0F0F0Fu);         // k0, k2, k4, k6
-        const uint32_t hi = nibbles_to_e4m3((x >> 4) & 0x0F0F0F0Fu);  // k1, k3, k5, k7
+        const uint32_t sign = x & 0x88888888u, one = sign >> 3;
+        const uint32_t mag = ((x & 0x77777777u) ^ (sign - one)) + one;
+        // bits 4 to 6 of a byte are clear in `sign`, whichever nibbles it counts
+        const uint32_t lo = (mag & kLow) | ((sign << 4) & ~kLow);   // k0, k2, k4, k6
+        const uint32_t hi = ((mag >> 4) & kLow) | (sign & ~kLow);   // k1, k3, k5, k7
         r[2 * i] = (int)__builtin_amdgcn_perm(hi, lo, 0x05010400u);
         r[2 * i + 1] = (int)__builtin_amdgcn_perm(hi, lo, 0x07030602u);
     }

@@ -40,23 +40,6 @@ __device__ __forceinline__ int wgt_slot(int row, int chunk)
     return row * 4 + (chunk ^ ((row >> 1 & 2) | (row >> 3 & 1)));
 }
 
-// 16 packed bytes -> 32 e4m3 codes of (v + 8) * 2^-9 in natural K order: 5
-// operations per 8 weights, where signed codes take 17.  The product starts
-// from -8 times the sum of the activations, which one more MFMA per slice
-// finds (a row of weights that are all -8, code 0x88).
-constexpr int kMinus8 = (int)0x88888888;
-__device__ __forceinline__ v8i int4_to_offset_fp8(const v4i& w)
-{
-    const v8i u = unpack_int4_u(w);
-    v8i r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r[2 * i] = (int)__builtin_amdgcn_perm((uint32_t)u[2 * i + 1], (uint32_t)u[2 * i], 0x05010400u);
-        r[2 * i + 1] = (int)__builtin_amdgcn_perm((uint32_t)u[2 * i + 1], (uint32_t)u[2 * i], 0x07030602u);
-    }
-    return r;
-}
-
 template <int MF, int NF, int D, int WAVES>
 struct RowsLds {
     static constexpr int kStage = NF * 1024 + MF * 2048;  // weights, then activations
@@ -150,12 +133,11 @@ __global__ __launch_bounds__(64 * WAVES) void dense_rows_kernel(const DenseArgs 
             acc[s][f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const float* const scales = (const float*)(mine + D * Lds::kStage);
     auto multiply = [&](const uint8_t* st, int gi) {  // group gi of the chunk
-        const v8i minus8 = {kMinus8, kMinus8, kMinus8, kMinus8, kMinus8, kMinus8, kMinus8, kMinus8};
         v8i b[NF];
         float sw[NF][4];
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            b[f] = int4_to_offset_fp8(*(const v4i*)(st + 1024 * f + 16 * wgt_slot(c16, q)));
+            b[f] = int4_to_fp8(*(const v4i*)(st + 1024 * f + 16 * wgt_slot(c16, q)));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 sw[f][i] = scales[(16 * f + 4 * q + i) * kChunk + gi];
@@ -167,10 +149,9 @@ __global__ __launch_bounds__(64 * WAVES) void dense_rows_kernel(const DenseArgs 
             const v8i av = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
             // the weight codes count units of 2^-9
             const float sa = 512.0f * scales[(16 * (NF + s) + c16) * kChunk + gi];
-            const v4f offset = mfma16x16x128(minus8, av, v4f{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
-                const v4f raw = mfma16x16x128(b[f], av, offset);
+                const v4f raw = mfma16x16x128(b[f], av, v4f{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     acc[s][f][i] = fmaf(sw[f][i], raw[i] * sa, acc[s][f][i]);

@@ -6,7 +6,7 @@
 // output and 128-group apply the group's two scales, and on this GPU they add
 // to the matrix core's time (counters of the 4096 x 7168 x 4096 product: matrix
 // core busy 36%, vector unit 49%).  So the int4 weights are not decoded in the K
-// loop (17 vector operations per 8 weights, twice over, since two waves share
+// loop (11 vector operations per 8 weights, twice over, since two waves share
 // each weight row): a first pass expands them once into e4m3 codes in the
 // workspace, laid out as the stages of the K loop (16 KB per 128 weight rows and
 // group, swizzled as they lie in LDS), and transposes both scale matrices.
