@@ -812,3 +812,17 @@ def test_gemm_epilogue_small_weights(dev, M, K, N):
     clear[:, 5::64] &= 0xF0   # k = 10 of 128
     clear[:, 37::64] &= 0x0F  # k = 75
     check_gemm((small, s, clear, sw))
+
+
+@pytest.mark.parametrize("M, K, N", [(1, 256, 40), (40, 256, 36), (300, 256, 100), (2500, 256, 2500)])
+def test_gemm_epilogue_largest_scale(dev, M, K, N):
+    """Activations up to the largest bf16 have scales up to 2^128 / 448: their
+    products stay finite where the result does."""
+    q, _, w, sw = gemm_inputs(dev, M, K, N)
+    top = torch.finfo(BF16).max / 448
+    s = torch.full((M, K // 128), top, device=dev)
+    s[1::2] = 2.0
+    few = torch.zeros_like(q)
+    few[:, ::32] = q[:, ::32]
+    assert float(ref.gemm_epilogue(few, s, w, sw)[0].abs().max()) < torch.finfo(BF16).max
+    check_gemm((few, s, w, sw))

@@ -147,8 +147,7 @@ __global__ __launch_bounds__(64 * WAVES) void dense_rows_kernel(const DenseArgs 
             const v4i a0 = *(const v4i*)(st + 1024 * NF + 16 * act_slot(16 * s + c16, 2 * q));
             const v4i a1 = *(const v4i*)(st + 1024 * NF + 16 * act_slot(16 * s + c16, 2 * q + 1));
             const v8i av = {a0[0], a0[1], a0[2], a0[3], a1[0], a1[1], a1[2], a1[3]};
-            // the weight codes count units of 2^-9
-            const float sa = 512.0f * scales[(16 * (NF + s) + c16) * kChunk + gi];
+            const float sa = scales[(16 * (NF + s) + c16) * kChunk + gi];
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
                 const v4f raw = mfma16x16x128(b[f], av, v4f{0.0f, 0.0f, 0.0f, 0.0f});
@@ -223,6 +222,11 @@ __global__ __launch_bounds__(64 * WAVES) void dense_rows_kernel(const DenseArgs 
                 up[0] += u.x, up[1] += u.y, up[2] += u.z, up[3] += u.w;
             }
         }
+        // the weight codes count units of 2^-9; not in the activations' scales,
+        // of which the largest (a bf16 maximum / 448) leaves no room for it
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] *= 512.0f, up[i] *= 512.0f;
         const int64_t m = m0 + 16 * s + c16, n = n0 + 16 * f + 4 * q;
         if (m < a.M)
             epilogue4(a, m, n, y, up, item == wave ? pre : load_epilogue4(a, m, n));
