@@ -826,3 +826,26 @@ def test_gemm_epilogue_largest_scale(dev, M, K, N):
     few[:, ::32] = q[:, ::32]
     assert float(ref.gemm_epilogue(few, s, w, sw)[0].abs().max()) < torch.finfo(BF16).max
     check_gemm((few, s, w, sw))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E, groups, kept", [(16, 2, 1), (64, 8, 1), (64, 8, 3), (256, 8, 1), (256, 8, 4), (512, 4, 1),
+                                             (512, 4, 2), (90, 6, 1), (1000, 8, 2), (128, 32, 5)])
+def test_route_groups_whose_sums_pass_32_bits(dev, score, E, groups, kept):
+    """Sums of two finite choices that 32 bits hold as an infinity: biases of
+    the type's lowest value as a mask, and of +-2e38 and +-3e38."""
+    size = E // groups
+    g = gen(dev, E)
+    x = torch.randn(40, E, generator=g, device=dev)
+    x[:20, :size] = -INF                       # the first group is empty
+    x[10:20, size + 1:2 * size] = -INF         # the next holds one expert
+    low = torch.finfo(FP32).min
+    biases = [torch.full((E,), low, device=dev), torch.full((E,), 3e38, device=dev)]
+    for values in ((low, -3e38, -2e38), (3e38, 2e38, 2.5e38), (low, 3e38, -INF), (low, 0.0, 3e38), (-2e38, 2e38, INF)):
+        b = torch.tensor(values, device=dev)[torch.randint(0, 3, (E,), generator=g, device=dev)]
+        biases += [b, b.reshape(groups, size)[:, :1].expand(-1, size).reshape(E).contiguous()]
+    for b in biases:
+        for top in (1, 2):
+            for rows in (x, x.to(BF16)):
+                check_route(rows, min(4, kept * size), score=score, bias=b, num_groups=groups, topk_groups=kept,
+                            group_top=top)

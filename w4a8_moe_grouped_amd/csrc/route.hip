@@ -49,7 +49,7 @@ __device__ __forceinline__ double in_sgprs(double c)
 }
 
 // exp to 64 bits for z in [-800, 709]: 2^n * e^r, |r| <= ln(2)/2, by the
-// Taylor sum to r^13/13! (the rest is below 4e-18)
+// Taylor sum to r^13/13! (the rest is below 4.3e-18)
 __device__ __forceinline__ double exp64(double z)
 {
     const double n = __builtin_rint(z * in_sgprs(1.4426950408889634));
@@ -600,7 +600,7 @@ __device__ __forceinline__ void rank_groups(float mine, int l, int run, float sl
         if ((N & (run - 1)) == 0) {
             const float v = dpp_f<kRor + N>(mine);
             better += (v > mine || (v == mine && l >= N)) ? 1 : 0;
-            close |= fabsf(v - mine) <= slack;  // two equal infinities (false here) tie in 64 bits too
+            close |= fabsf(v - mine) <= slack;  // false for two equal infinities
         }
         rank_groups<N + 1>(mine, l, run, slack, better, close);
     }
@@ -750,8 +750,13 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a)
             // of any two groups of the row (infinite where one is: all close)
             slack = __uint_as_float(row_max(v1 > ninf ? __float_as_uint(slack) : 0));
         }
+        const float value = two ? v1 + v2 : v1;
+        // equal infinities tie in 64 bits too, but for a sum of finite choices
+        // that only 32 bits cannot hold
+        if (two)
+            close = fabsf(value) == __builtin_inff() && fabsf(v1) < __builtin_inff() && fabsf(v2) < __builtin_inff();
         int better = 0;
-        rank_groups<1>(two ? v1 + v2 : v1, l, run, slack, better, close);
+        rank_groups<1>(value, l, run, slack, better, close);
         open = better < a.kept;
     }
 #pragma unroll
