@@ -849,3 +849,36 @@ def test_route_groups_whose_sums_pass_32_bits(dev, score, E, groups, kept):
             for rows in (x, x.to(BF16)):
                 check_route(rows, min(4, kept * size), score=score, bias=b, num_groups=groups, topk_groups=kept,
                             group_top=top)
+
+
+@pytest.mark.parametrize("T, H", [(513, 520), (600, 1000), (517, 7168), (514, 8192), (530, 2085), (600, 512), (513, 513)])
+@pytest.mark.parametrize("xt, rt, pt", [(BF16, BF16, BF16), (BF16, FP32, FP32), (FP32, BF16, FP32)])
+def test_norm_many_rows(dev, T, H, xt, rt, pt):
+    """More rows than get a workgroup of one chunk a thread, every row its own."""
+    d = norm_inputs(dev, T, H, xt, rt, pt, seed=40)
+    x, r = padded(d["x"], 3), padded(d["residual"], 5)
+    for gate in ("channel", "token", "full"):
+        g = padded(d["full"], 1) if gate == "full" else d[gate]
+        kw = dict(post_weight=d["post"], gate=g, residual_scale=0.5, pre_weight=d["pre"])
+        y = torch.full((T, H + 1), 3.0, dtype=BF16, device=dev)
+        check_norm(x, r, got=w4.norm_residual(x, r, out=y[:, :H], **kw), **kw)
+        assert bool((y[:, H:] == 3).all())
+        if H % 128 == 0:
+            check_norm(x, r, quantize=True, **kw)
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+@pytest.mark.parametrize("T, E, k, groups, kept", [(4097, 64, 6, 8, 3), (4099, 40, 4, 1, 1), (4110, 33, 12, 3, 2), (4111, 160, 8, 4, 2)])
+def test_route_many_tokens(dev, dtype, T, E, k, groups, kept):
+    """More tokens than get a workgroup of one wave, every row its own: random
+    ones, near ties, and padding that begins inside the last workgroup."""
+    g = gen(dev, T)
+    x = torch.randn(T, E, generator=g, device=dev)
+    x[1::3] = 1 + torch.finfo(dtype).eps * torch.randint(0, 9, (T, E), generator=g, device=dev)[1::3]
+    x[7::50] = -INF
+    x = padded(x.to(dtype), 5)
+    bias = 0.2 * torch.randn(E, generator=g, device=dev)
+    for score, b, num in (("sigmoid", None, T), ("sigmoid", bias, T - 1), ("softmax", torch.zeros_like(bias), T - 6),
+                          ("softmax", None, 4094)):
+        n = torch.tensor([num], dtype=torch.int32, device=dev)
+        check_route(x, k, score=score, bias=b, num_groups=groups, topk_groups=kept, num_tokens=n, renormalize=b is None)
