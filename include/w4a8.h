@@ -538,9 +538,12 @@ int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* resid
  *                that may run at once, replays of captured graphs among them,
  *                need one each
  * M >= 0 (M == 0 launches nothing), N > 0, K > 0 (INVALID_ARG otherwise), K %
- * 128 == 0, K <= 2^22, M, R < 2^31, launches below 2^32 threads (met by up to
- * 2^33 outputs with M % 32 == 0 and 2^36 weights), pointers 16-byte aligned
- * (UNSUPPORTED otherwise).  Operands may exceed 2^32 bytes.
+ * 128 == 0, K <= 2^22, M, R < 2^31, launches below 2^32 threads, pointers
+ * 16-byte aligned (UNSUPPORTED otherwise).  The query tells whether the launches
+ * fit.  They do where R <= 2^28 - 32, ceil(M/32) * ceil(R/64) < 2^24,
+ * ceil(R/128) * ceil(K/256) <= 2^21 and ceil(M/128) * ceil(K/1024) <= 2^22: narrow
+ * weights take as many threads a row as 64 rows of them.  Operands may exceed
+ * 2^32 bytes.
  */
 #define W4A8_ACT_NONE 0
 #define W4A8_ACT_RELU 1

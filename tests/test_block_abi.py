@@ -4,6 +4,7 @@ binding, and the plain 64-bit forms the GPU tests compare with."""
 import ctypes
 import math
 import os
+import random
 
 import pytest
 import torch
@@ -176,3 +177,27 @@ def test_gemm_epilogue_without_workspace_bytes(L):
     assert _gemm(L, K=2048, N=7168, ldo=7168, nbytes=0) == OK
     assert _gemm(L, M=4, a=None, nbytes=0) == INVALID  # not taken for a query
     assert _gemm(L, M=4, a=None, ws=None, nbytes=0) == OK
+
+
+@pytest.mark.parametrize("M, K, N, act, want", [
+    # 32 rows of one weight row take as many threads as of 64
+    (1 << 29, 128, 1, 0, UNSUPPORTED), (1 << 29, 128, 16, 0, UNSUPPORTED), ((1 << 29) - 32, 128, 64, 0, OK),
+    (16, 128, (1 << 28) - 32, 0, OK)])
+def test_gemm_epilogue_threads_of_narrow_weights(L, M, K, N, act, want):
+    assert _gemm(L, M=M, K=K, N=N, act=act, ldo=N, ws=None) == want
+
+
+def test_gemm_epilogue_sizes_that_always_fit(L):
+    """The sizes that include/w4a8.h promises, at random over the whole range."""
+    rng = random.Random(5)
+    up = lambda a, b: -(-a // b)  # noqa: E731
+    checked = 0
+    for _ in range(20000):
+        act = rng.choice([0, 5])
+        M, N, G = (int(2 ** rng.uniform(0, top)) for top in (30.9, 29.9 if act else 30.9, 15))
+        R, K = (2 * N if act else N), 128 * G
+        if R <= 2 ** 28 - 32 and up(M, 32) * up(R, 64) < 2 ** 24 and up(R, 128) * up(K, 256) <= 2 ** 21 \
+                and up(M, 128) * up(K, 1024) <= 2 ** 22:
+            checked += 1
+            assert _gemm(L, M=M, K=K, N=N, act=act, ldo=N, ws=None) == OK, (M, K, N, act)
+    assert checked > 1000
