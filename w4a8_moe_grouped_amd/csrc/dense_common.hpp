@@ -48,8 +48,9 @@ __device__ __forceinline__ float silu(float y)
     return times_sigmoid(y, y);
 }
 
-// erfc(z), z >= 0, to 4e-7, and to 2e-6 of its value up to z = 4: t e^(P(t) -
-// z^2) with t = 1/(1 + z/2) and P the degree-10 Chebyshev fit of ln(erfc(z)
+// erfc(z), z >= 0, to 4e-7, and to 2e-6 of its value up to z = 4 (8e-6 far out):
+// t e^(P(t) - z^2) with t = 1/(1 + z/2), the form that Press et al. publish in
+// Numerical Recipes, and P a degree-10 Chebyshev fit of its own to ln(erfc(z)
 // e^(z^2) / t) over 0 < t <= 1 (the library's erfcf took 2 us of a 10 us call)
 __device__ __forceinline__ float erfc_positive(float z)
 {

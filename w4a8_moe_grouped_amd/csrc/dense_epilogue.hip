@@ -13,8 +13,12 @@
 // kept a CU's address unit busy for 4.5 us of a 12 us call.)  The 8 sums of
 // an output meet in LDS, in wave order.
 //
-// M 1, K 7168, R 4096: 7.0 us for 15.6 MB (2.2 TB/s; 4.1 us of it at K = 128:
-// launch, one load, the sums); M 64, K 2048, R 7168 with a residual: 7.0 us.
+// M 1, K 7168, R 4096: 7.8 us for 15.6 MB (2.0 TB/s; 3.3 us of it at K = 128:
+// launch, one load, the sums); M 64, K 2048, R 7168: 6.1 us.  The weights become
+// signed codes, as in the tiles: codes of v + 8, which take half the decode (6.7
+// and 5.8 us), add 8 times the activations to what the matrix instruction sums
+// in 13 bits and take them off again, so that small weights lose bits to large
+// activations and a weight of 0 does not give 0.
 //
 // The weights are the first MFMA operand, so a lane holds four consecutive
 // outputs of one row, which the epilogue reads and writes as one access.  With
@@ -168,7 +172,7 @@ __global__ __launch_bounds__(64 * WAVES) void dense_rows_kernel(const DenseArgs 
         int st = 0, i = 0;
         if constexpr (D % 2 == 0 && D > 2) {
             // two groups at a time: one's matrix products run under the other's
-            // decode (1 x 7168 x 4096: 7.4 us against 7.9)
+            // decode (1 x 7168 x 4096: 7.8 us against 8.2)
             for (; i + 1 < n; i += 2) {
                 if (n - 2 - i >= D - 2)
                     wait_vmcnt<(D - 2) * kLoads>();
@@ -275,10 +279,10 @@ hipError_t launch_dense_epilogue(const DenseArgs& a, void* ws, hipStream_t s)
     // what counts is how many a CU holds (32 to 44 KB of LDS each, ring of one
     // stage), so that one's loads run under another's products, and from about
     // three rounds on wider ones, which load fewer activations.  Measured (us;
-    // <slices, fragments, ring, waves>): M 64, K 7168, R 4096 <2,2,1,8> 9.7,
-    // <2,2,1,4> 13.0, <2,4,1,4> 16.0; M 64, K 2048, R 7168 7.9 / 7.1 / 8.5; M 300
-    // 22.9 / 18.9 / 16.3; M 512, K 7168, R 2048 25.1 / 24.2 / 19.8; a ring of two
-    // stages with <2,4> and 8 waves takes 8.6, 27.5 and 24.2 on the last three.
+    // <slices, fragments, ring, waves>): M 64, K 7168, R 4096 <2,2,1,8> 9.6,
+    // <2,2,1,4> 13.3, <2,4,1,4> 17.9; M 64, K 2048, R 7168 7.1 / 6.3 / 7.9; M 300
+    // 23.4 / 19.5 / 18.3; M 512, K 7168, R 2048 28.0 / 27.3 / 26.4; a ring of two
+    // stages with <2,4> and 8 waves takes 7.6, 31.1 and 30.0 on the last three.
     if (a.M <= 16)
         return launch_rows<1, 2, 4, 8>(a, s);
     const int64_t R = a.act == W4A8_ACT_SWIGLU ? 2 * a.N : a.N;

@@ -3,9 +3,10 @@
 //
 // The product runs on the fp8 matrix instruction, whose operands are bytes,
 // and what limits it is the vector work around it: two fp32 operations per
-// output and 128-group apply the group's two scales, and on this GPU they add
-// to the matrix core's time (counters of the 4096 x 7168 x 4096 product: matrix
-// core busy 36%, vector unit 49%).  So the int4 weights are not decoded in the K
+// output and 128-group apply the group's two scales, and in this schedule they
+// hardly overlap the matrix core's (counters of the 4096 x 7168 x 4096 product:
+// matrix core busy 37% of the cycles, other vector instructions 43%, neither a
+// fifth).  So the int4 weights are not decoded in the K
 // loop (11 vector operations per 8 weights, twice over, since two waves share
 // each weight row): a first pass expands them once into e4m3 codes in the
 // workspace, laid out as the stages of the K loop (16 KB per 128 weight rows and
@@ -408,8 +409,10 @@ int64_t weight_rows(int64_t N, int act)
 // The tiles with their first pass (a launch, 5 us and 0.38 ps a weight)
 // against the few-rows kernel, whose workgroups of 32 rows x 64 weight rows
 // decode the weights again for every 32 rows (4.2 ns + 3.67 ps K each, over
-// all CUs).  Both sides measured: 768 x 7168 x 4096 73 us and 51, 1024 x 2048 x
-// 7168 41 and 46, 1500 x 2048 x 2048 29 and 20, 4096 x 128 x 4096 22 and 38.
+// all CUs; the second is 4.5 on long K, which changes the choice only near the
+// border: 2048 x 7168 x 2048 74 us and 79).  Both sides measured: 768 x 7168 x 4096
+// 74 us and 60, 1024 x 2048 x 7168 41 and 46, 1500 x 2048 x 2048 31 and 23, 4096 x
+// 128 x 4096 22 and 40.
 bool use_dense_tiles(int64_t M, int64_t K, int64_t N, int act)
 {
     const int64_t R = weight_rows(N, act);

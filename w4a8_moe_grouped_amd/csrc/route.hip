@@ -21,8 +21,8 @@
 // DPP maximum over the wave (no LDS) and one ballot per slot.
 //
 // Bound: instruction issue.  32768 tokens, 256 experts in 8 groups, top 8,
-// sigmoid and bias: 20 us, 1.8 TB/s of logits; 194 vector operations a token
-// (775 per wave of four), which alone are 10.5 us of every SIMD; the exact kernel
+// sigmoid and bias: 20 us, 1.8 TB/s of logits; 195 vector operations a token
+// (780 per wave of four), which alone are 10.5 us of every SIMD; the exact kernel
 // takes 52 us.  How many waves a CU holds does not matter (12 to 24: 20.4 to
 // 22.8 us), nor does loading the next tokens ahead.  64 tokens: 5 us, all
 // latency.
