@@ -882,3 +882,31 @@ def test_route_many_tokens(dev, dtype, T, E, k, groups, kept):
                           ("softmax", None, 4094)):
         n = torch.tensor([num], dtype=torch.int32, device=dev)
         check_route(x, k, score=score, bias=b, num_groups=groups, topk_groups=kept, num_tokens=n, renormalize=b is None)
+
+
+@pytest.mark.parametrize("M, K, N", [(1, 512, 48), (40, 512, 48), (300, 512, 100), (4096, 256, 4096)])
+def test_gemm_epilogue_keeps_13_bits_below_the_largest_product(dev, M, K, N):
+    """Large activations under weights of +-1, whose products cancel, and small
+    ones beside them: the matrix instruction cuts a product to 2^-13 of the
+    largest of its eight neighbours in K, so each eight are off by at most 7
+    2^-13 of that."""
+    g = gen(dev, M + N)
+    s = 0.5 + torch.rand(M, K // 128, generator=g, device=dev)
+    sw = 0.002 + 0.018 * torch.rand(N, K // 128, generator=g, device=dev)
+    for small, unit in ((0x20, 1), (0x20, 0), (0x28, 0), (0x18, 0)):
+        # codes of about 2^-3, 2^-2 and 2^-4; +448 and -448 in turn at one place of every eight
+        q = small + torch.randint(0, 1 if unit else 8, (M, K), generator=g, device=dev, dtype=torch.uint8)
+        q[:, 3::16], q[:, 11::16] = 0x7E, 0xFE
+        v = torch.ones(N, K, dtype=torch.uint8, device=dev) if unit else \
+            torch.randint(0, 8, (N, K), generator=g, device=dev, dtype=torch.uint8)
+        v[:, 3::8] = 1
+        v[::2, 3::8] = 15  # -1
+        w = v[:, ::2] | v[:, 1::2] << 4
+        out = w4.gemm_epilogue(q, s, w, sw).double()
+        want, _ = ref.gemm_epilogue(q, s, w, sw)
+        # the eights' largest products: 448 times 1, the small ones' are below 4
+        top = torch.full((N, K // 8), 448.0, dtype=torch.float64, device=dev)
+        err = 7 * 2.0 ** -13 * (s.double() @ (top.reshape(N, -1, 16).sum(-1) * sw.double()).t().contiguous())
+        err = err + (2 * (K // 128) + 2) * U * (ref.dequant(q, s).abs() @ ref.int4(w, sw).abs().t().contiguous())
+        diff = (out - want).abs()
+        assert bool((diff <= err + 2.0 ** -8 * (want.abs() + err)).all()), float((diff - err - 2.0 ** -8 * want.abs()).max())

@@ -5,10 +5,10 @@
 // and what limits it is the vector work around it: two fp32 operations per
 // output and 128-group apply the group's two scales, and in this schedule they
 // hardly overlap the matrix core's (counters of the 4096 x 7168 x 4096 product:
-// matrix core busy 37% of the cycles, other vector instructions 43%, neither a
-// fifth).  So the int4 weights are not decoded in the K
-// loop (11 vector operations per 8 weights, twice over, since two waves share
-// each weight row): a first pass expands them once into e4m3 codes in the
+// matrix core busy 36% of the cycles, other vector instructions 42%, neither a
+// fifth).  So the int4 weights are not decoded in the K loop
+// (13 vector operations per 8 weights, twice over, since two waves share each
+// weight row): a first pass expands them once into e4m3 codes in the
 // workspace, laid out as the stages of the K loop (16 KB per 128 weight rows and
 // group, swizzled as they lie in LDS), and transposes both scale matrices.
 //
@@ -24,7 +24,7 @@
 // ranges, one per XCD, so that the tiles that run at the same time on one XCD
 // share their rows and weights in its L2.
 //
-// 4096 x 7168 x 4096 with SwiGLU, N(0, 1) activations: the tiles 127 to 150 us
+// 4096 x 7168 x 4096 with SwiGLU, N(0, 1) activations: the tiles 125 to 150 us
 // (1.6 to 1.9 PFLOP/s, by the power the operands draw), the first pass 13 us;
 // torch's bf16 product of that shape's square runs at 1.2 to 1.3 PFLOP/s, its fp8
 // product with one scale per tensor at 3.0.
@@ -105,7 +105,6 @@ __global__ __launch_bounds__(256) void dense_expand_kernel(const TileArgs t)
     const int64_t row = weights ? unit_weight_row(d, u, r) : min(u * kUnit + r, d.M - 1);
     const float* src = (weights ? d.sw : d.sa) + row * t.G;
     float* dst = (weights ? t.swt : t.sat) + u * t.G * kUnit + r;
-    const float mul = weights ? 512.0f : 1.0f;  // the codes count units of 2^-9
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -113,7 +112,7 @@ __global__ __launch_bounds__(256) void dense_expand_kernel(const TileArgs t)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (g0 + i < t.G)
-            dst[(int64_t)(g0 + i) * kUnit] = mul * v[i];
+            dst[(int64_t)(g0 + i) * kUnit] = v[i];
 }
 
 namespace {
@@ -254,14 +253,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_tile_kernel(const TileA
         for (int f = 0; f < 4; ++f)
             sw[f] = *(const float4*)(psw + 64 * f);
         // slice s is multiplied while slice s - 1 gets its scales: the vector
-        // unit works on results that are already there
+        // unit works on results that are already there.  The scales meet first:
+        // the largest activation scale has no room for the sum alone
         v4f raw[4];
         float sa_raw = 0.0f;  // scale of the rows in raw
         auto promote = [&](int s, int f) {
-            acc[s][f][0] = fmaf(sw[f].x, raw[f][0] * sa_raw, acc[s][f][0]);
-            acc[s][f][1] = fmaf(sw[f].y, raw[f][1] * sa_raw, acc[s][f][1]);
-            acc[s][f][2] = fmaf(sw[f].z, raw[f][2] * sa_raw, acc[s][f][2]);
-            acc[s][f][3] = fmaf(sw[f].w, raw[f][3] * sa_raw, acc[s][f][3]);
+            acc[s][f][0] = fmaf(raw[f][0], sw[f].x * sa_raw, acc[s][f][0]);
+            acc[s][f][1] = fmaf(raw[f][1], sw[f].y * sa_raw, acc[s][f][1]);
+            acc[s][f][2] = fmaf(raw[f][2], sw[f].z * sa_raw, acc[s][f][2]);
+            acc[s][f][3] = fmaf(raw[f][3], sw[f].w * sa_raw, acc[s][f][3]);
         };
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
