@@ -622,6 +622,161 @@ int w4a8_fused_moe_workspace_layout(int64_t T, int64_t H, int64_t topk,
  */
 int w4a8_fused_moe_stage_events(void* const* events, int n);
 
+/*
+ * w4a8_gemm_fp8 -- the dense linear of the layers that keep fp8 weights with
+ * block scales (SGLang PR #7762, "Model Info": dense layers use FP8 block
+ * scaling), with the epilogue of w4a8_gemm_epilogue:
+ *   out[m, n] = bf16(act(y[m, n] + bias[n]) + residual[m, n]),
+ *   y[m, n]   = sum_g a_scale[m, g] * b_scale[n / 128, g] * sum_{k in g} dec(a[m, k]) * dec(b[n, k])
+ *   a_e4m3, a_scales   [M, K] codes and [M, K/128] fp32 scales, as
+ *                      w4a8_quantize_act and w4a8_norm_residual write them
+ *   b_e4m3             [R, K] e4m3 codes, R = N (2N with SwiGLU: gate rows, then up rows)
+ *   b_scales           [ceil(R/128), K/128] fp32, one for each 128 x 128 block
+ *   bias, activation, residual, out, ld_*, workspace   as w4a8_gemm_epilogue
+ * K % 128 == 0, and with SwiGLU N % 128 == 0 (gate and up rows have blocks of
+ * their own); other limits, workspace query and errors as w4a8_gemm_epilogue;
+ * K <= 2^22.  A product is off by what the fp8 matrix instruction cuts (2^-13
+ * of the largest of eight neighbours in K); sums over groups, scales and the
+ * epilogue are in fp32, with one rounding at the end.
+ */
+int w4a8_gemm_fp8(const uint8_t* a_e4m3, const float* a_scales, int64_t M, int64_t K,
+                  const uint8_t* b_e4m3, const float* b_scales, int64_t N, const void* bias,
+                  int bias_type, int activation, const void* residual_bf16, int64_t ld_residual,
+                  void* out_bf16, int64_t ld_out, void* workspace, size_t* workspace_bytes,
+                  hipStream_t stream);
+
+/*
+ * w4a8_rope_frequencies -- the angle per position of each rotated pair,
+ * frequencies[i] for i < rotary_dim / 2, in 64 bits.  With R = rotary_dim and
+ * f_i = base^(-2i / R):
+ *   W4A8_ROPE_PLAIN   f_i
+ *   W4A8_ROPE_LINEAR  f_i / factor
+ *   W4A8_ROPE_NTK     the same with base * factor^(R / (R - 2))  (R > 2)
+ *   W4A8_ROPE_YARN    f_i / factor * r + f_i * (1 - r), r = clamp((i - lo) /
+ *                     max(hi - lo, 0.001), 0, 1), lo = max(floor(c(beta_fast)), 0), hi =
+ *                     min(ceil(c(beta_slow)), R - 1), c(b) = R * ln(original_length /
+ *                     (2 pi b)) / (2 ln base): pairs that turn more than
+ *                     beta_fast times over the original length stay, those
+ *                     below beta_slow turns are interpolated.  (The factor on
+ *                     the logits that goes with it is `magnitude` of the calls
+ *                     below, usually 0.1 ln(factor) + 1.)
+ * rotary_dim even, 2..256, base > 1, factor > 0 and finite, beta_fast >= beta_slow > 0,
+ * original_length > 0 (the last three with YaRN only); INVALID_ARG otherwise.
+ * frequencies is 8-byte aligned.
+ */
+#define W4A8_ROPE_PLAIN 0
+#define W4A8_ROPE_LINEAR 1
+#define W4A8_ROPE_NTK 2
+#define W4A8_ROPE_YARN 3
+int w4a8_rope_frequencies(int64_t rotary_dim, double base, int scaling, double factor,
+                          double original_length, double beta_fast, double beta_slow,
+                          double* frequencies, hipStream_t stream);
+
+/*
+ * w4a8_rope -- rotary positions.  Of each head's D = head_dim elements the
+ * first R = rotary_dim are R/2 pairs, pair i of token t turned by the angle
+ * positions[t] * frequencies[i]:
+ *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos)
+ *   interleaved 0: a, b = elements i and i + R/2;  else 2i and 2i + 1
+ * The other D - R elements are copied.  The angle is taken in 64 bits, sine
+ * and cosine are good to 2e-7 at any position, and every output is rounded
+ * once from fp32.
+ *   x, out        [T, heads, D] of `type` (fp32, bf16 or fp16), element (t, h, d) at
+ *                 t * token_stride + h * head_stride + d; out may be x itself
+ *                 (same strides) and does not overlap it otherwise
+ *   positions     [T] int32
+ *   frequencies   [R/2] fp64, or NULL with rotary_dim 0 (a copy)
+ * T, heads >= 0; D a multiple of 8 up to 256, R even, 0 <= R <= D; strides
+ * non-negative multiples of 8; T <= 2^25, heads <= 4096 (UNSUPPORTED beyond).
+ */
+int w4a8_rope(const void* x, int type, int64_t T, int64_t heads, int64_t head_dim,
+              int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+              const double* frequencies, int64_t rotary_dim, int interleaved, float magnitude,
+              void* out, int64_t out_token_stride, int64_t out_head_stride, hipStream_t stream);
+
+/*
+ * A paged cache of keys and values: num_pages pages of page_size tokens.
+ * Element (page, token, head, d) of k lies at page * k_page_stride + token *
+ * k_token_stride + head * k_head_stride + d (elements; the same for v), so
+ * both [pages, tokens, heads, D] and [pages, heads, tokens, D] serve, and
+ * views of one buffer.  With type W4A8_TYPE_E4M3 the elements are codes and
+ * each token and head has one fp32 scale, k_scales and v_scales
+ * [num_pages, kv_heads, page_size]; they are NULL for bf16 and fp16.  Codes
+ * need no more than 8-byte alignment; strides are non-negative multiples of 8.
+ * The struct itself is in host memory.
+ */
+#define W4A8_TYPE_E4M3 3
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scales;
+    float* v_scales;
+    int type; /* W4A8_TYPE_BF16, W4A8_TYPE_FP16 or W4A8_TYPE_E4M3 */
+    int64_t num_pages, page_size, kv_heads, head_dim;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+} w4a8_kv_cache;
+
+/*
+ * w4a8_kv_append -- writes the keys and values of T tokens into a paged cache,
+ * with the rotation of w4a8_rope on the keys, and on the queries beside them,
+ * in one launch.
+ *   q             [T, q_heads, D] or NULL; q_out the same, rotated (may be q itself)
+ *   k, v          [T, kv_heads, D]; k is rotated, v is not
+ *   type          of q, k, v and q_out: W4A8_TYPE_BF16 or W4A8_TYPE_FP16, the
+ *                 cache's own unless that is e4m3, which takes both
+ *   slots         [T] int64: token t goes to place slots[t] % page_size of
+ *                 page slots[t] / page_size; a slot outside the cache (-1: the
+ *                 padding of a batch) is not written, its query is rotated all
+ *                 the same.  Where two tokens of a call name one slot, the
+ *                 slot holds a mixture of them
+ *   positions, frequencies, rotary_dim, interleaved, magnitude   as w4a8_rope
+ *                 (positions may be NULL with rotary_dim 0)
+ * e4m3: the D elements of a head, rotated and not rounded before, are one
+ * block of the quantisation rule above: scale = max(amax, 1e-10) / 448, code =
+ * e4m3(clamp(x * 448 / max(amax, 1e-10))); a NaN shows in the scale.  All
+ * else in the cache stays as it was.
+ * D = cache->head_dim; strides are non-negative multiples of 8; sizes and
+ * errors as w4a8_rope, and q_heads + 2 * kv_heads <= 4096.  slots is 8-byte aligned.
+ */
+int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                   const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                   int64_t v_token_stride, int64_t v_head_stride, int type, int64_t T,
+                   const int64_t* slots, const int32_t* positions, const double* frequencies,
+                   int64_t rotary_dim, int interleaved, float magnitude, const w4a8_kv_cache* cache,
+                   void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                   hipStream_t stream);
+
+/*
+ * w4a8_attn_decode -- attention of one new token of each of B sequences over
+ * the paged cache.  Sequence b holds seq_lens[b] tokens, its new one last;
+ * token j lies at place j % page_size of page page_table[b, j / page_size].
+ * With window w > 0 the last w of them are seen, else all:
+ *   s_j = scale * q[b, h] . k_j,  out[b, h] = sum_j softmax(s)_j v_j,
+ *   lse[b, h] = ln sum_j e^s_j
+ * over kv head h / (q_heads / kv_heads).  Tokens whose page number is outside
+ * 0..num_pages - 1, or past the table, hold nothing and are left out; where
+ * nothing is left (a length of 0 or less), out is 0 and lse -inf.
+ *   q, out        [B, q_heads, D] of q_type: bf16 or fp16, the cache's type, or
+ *                 bf16 with an e4m3 cache; no overlap
+ *   page_table    [B, max_pages] int32, row stride ld_table;  seq_lens [B] int32
+ *   lse           [B, q_heads] fp32, or NULL
+ *   workspace     partial results of sequences that are cut into parts (query
+ *                 with NULL: a function of B, q_heads, kv_heads, D, max_pages
+ *                 and page_size)
+ * Scores and sums are in fp32; the softmax weights are rounded to q_type
+ * before they meet the values.  How a batch is cut follows all its lengths, so
+ * the order of a row's sums depends on the batch.
+ * D = cache->head_dim: a multiple of 8 up to 256; q_heads a multiple of
+ * kv_heads (INVALID_ARG otherwise); strides non-negative multiples of 8, B <=
+ * 65536, q_heads <= 4096, max_pages * page_size <= 2^30 (UNSUPPORTED otherwise).
+ */
+int w4a8_attn_decode(const void* q, int q_type, int64_t B, int64_t q_heads, int64_t q_seq_stride,
+                     int64_t q_head_stride, const w4a8_kv_cache* cache, const int32_t* page_table,
+                     int64_t max_pages, int64_t ld_table, const int32_t* seq_lens, float scale,
+                     int64_t window, void* out, int64_t out_seq_stride, int64_t out_head_stride,
+                     float* lse, void* workspace, size_t* workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,8 +3,8 @@
     python -m w4a8_moe_grouped_amd.build
 
 Every .hip file under csrc/ is compiled to an object under _build/ (in
-parallel), then linked into w4a8_moe_grouped_amd/libw4a8.so.  csrc/binding.cpp,
-the native half of the Python binding's short calls, becomes
+parallel), then linked into w4a8_moe_grouped_amd/libw4a8.so.  csrc/binding.cpp
+and binding_attn.cpp, the native half of the Python binding's short calls, become
 w4a8_moe_grouped_amd/_binding.so beside it (host code only, against torch's
 headers).
 """
@@ -57,13 +57,14 @@ def _build_binding() -> None:
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
-    for path in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]:
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
+    for path in cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(rocm, "include")]:
         cmd += ["-isystem", path]
-    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", lib_dir, "-lc10", "-ltorch_cpu", "-ltorch_hip",
-            "-ltorch_python"]
+    cmd += ["-I", INCLUDE, *(os.path.join(CSRC, f) for f in ("binding.cpp", "binding_attn.cpp")), "-o", tmp,
+            "-L", lib_dir, "-lc10", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("g++ failed for binding.cpp:\n%s\n%s" % (" ".join(cmd), r.stderr))
+        raise RuntimeError("g++ failed for the binding:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, BINDING)
 
 

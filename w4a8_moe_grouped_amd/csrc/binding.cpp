@@ -1,25 +1,18 @@
 // binding.cpp -- the host side of the Python calls whose kernels take a few
-// microseconds (moe_route, norm_residual, gemm_epilogue): argument checks,
-// output allocation and the call into libw4a8, in one native call.  Through
-// ctypes the same steps took 8 to 11 us of host time, more than the kernels of
-// a decode batch.  lib.py holds the signatures and the documentation.
+// microseconds (moe_route, norm_residual, gemm_epilogue; binding_attn.cpp has
+// those of the attention half): argument checks, output allocation and the
+// call into libw4a8, in one native call.  Through ctypes the same steps took 8
+// to 11 us of host time, more than the kernels of a decode batch.  lib.py holds
+// the signatures and the documentation.
 //
 // The module is given, once, the exception to raise, torch's accessor of the
-// current raw stream and the addresses of the three exports.
-#include <Python.h>
+// current raw stream and the addresses of the exports.
+#include "binding_util.hpp"
 
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <ATen/hip/EmptyTensor.h>
-#include <c10/core/DeviceGuard.h>
-
-#include <stdexcept>
-#include <string>
-#include <vector>
+using namespace w4a8_binding;
 
 namespace {
 
-typedef void* Stream;
 typedef int (*RouteFn)(const void*, int, int64_t, int64_t, int64_t, const float*, int, int64_t, int64_t, int, int64_t,
                        int, float, const int32_t*, int32_t*, float*, Stream);
 typedef int (*NormFn)(const void*, int, int64_t, const void*, int, int64_t, int64_t, int64_t, int, const void*,
@@ -27,190 +20,10 @@ typedef int (*NormFn)(const void*, int, int64_t, const void*, int, int64_t, int6
                       uint8_t*, float*, Stream);
 typedef int (*GemmFn)(const uint8_t*, const float*, int64_t, int64_t, const uint8_t*, const float*, int64_t, const void*,
                       int, int, const void*, int64_t, void*, int64_t, void*, size_t*, Stream);
-typedef const char* (*StatusFn)(int);
 
-PyObject *g_error = nullptr, *g_raw_stream = nullptr;
 RouteFn g_route = nullptr;
 NormFn g_norm = nullptr;
 GemmFn g_gemm = nullptr;
-StatusFn g_status = nullptr;
-
-constexpr int64_t kGroup = 128;
-constexpr int kActSwiglu = 5;
-
-// named by a call that needs no workspace, and never followed: null would ask
-// for the size, and null is the address of every empty tensor
-alignas(16) char g_no_workspace[16];
-
-// the message of a W4A8Error
-struct Refused : std::runtime_error {
-    using std::runtime_error::runtime_error;
-};
-// a Python error that is set already
-struct Raised {};
-
-[[noreturn]] void refuse(const std::string& what)
-{
-    throw Refused(what);
-}
-
-// a tensor argument, or null for None
-const at::Tensor* tensor(PyObject* o, const char* what)
-{
-    if (o == Py_None)
-        return nullptr;
-    if (!THPVariable_Check(o))
-        refuse(std::string(what) + " must be a tensor");
-    return &THPVariable_Unpack(o);
-}
-const at::Tensor& required(PyObject* o, const char* what)
-{
-    const at::Tensor* t = tensor(o, what);
-    if (t == nullptr)
-        refuse(std::string(what) + " must be a tensor");
-    return *t;
-}
-int64_t integer(PyObject* o)
-{
-    const long long v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred())
-        throw Raised();
-    return v;
-}
-float number(PyObject* o)
-{
-    const double v = PyFloat_AsDouble(o);
-    if (v == -1.0 && PyErr_Occurred())
-        throw Raised();
-    return (float)v;
-}
-bool truth(PyObject* o)
-{
-    const int v = PyObject_IsTrue(o);
-    if (v < 0)
-        throw Raised();
-    return v != 0;
-}
-
-std::string name(at::IntArrayRef s)
-{
-    std::string r = "[";
-    for (size_t i = 0; i < s.size(); ++i)
-        r += (i ? ", " : "") + std::to_string(s[i]);
-    return r + "]";
-}
-
-int type_of(const at::Tensor& t, bool half = false)
-{
-    switch (t.scalar_type()) {
-    case at::kFloat: return 0;
-    case at::kBFloat16: return 1;
-    case at::kHalf:
-        if (half)
-            return 2;
-        break;
-    default: break;
-    }
-    refuse(std::string("unsupported tensor type ") + c10::toString(t.scalar_type()));
-}
-
-// the address of a tensor that must lie on `device` (null: none)
-void* addr(const at::Tensor* t, const at::Device& device)
-{
-    if (t == nullptr)
-        return nullptr;
-    if (t->device() != device)
-        refuse("all tensors must be on one GPU");
-    return t->data_ptr();
-}
-
-// row stride of a [rows, cols] tensor with unit column stride
-int64_t row_stride(const at::Tensor& t, int64_t rows, int64_t cols, const char* what)
-{
-    if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
-        refuse(std::string(what) + " must be " + name({rows, cols}) + ", not " + name(t.sizes()));
-    if (t.stride(1) != 1 && cols > 1)
-        refuse(std::string(what) + " must have unit column stride");
-    return rows > 1 ? t.stride(0) : cols;
-}
-
-void whole(const at::Tensor& t, at::IntArrayRef shape, at::ScalarType type, const char* what)
-{
-    if (t.sizes() != shape || t.scalar_type() != type || !t.is_contiguous())
-        refuse(std::string(what) + " must be a contiguous " + c10::toString(type) + " tensor of shape " + name(shape));
-}
-
-// an output: torch's caching allocator, without the way through its dispatcher
-at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Device& device)
-{
-    return at::Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
-}
-
-void need_gpu(const at::Tensor& t)
-{
-    if (!t.is_cuda())
-        refuse("all tensors must be on the GPU");
-}
-
-Stream stream_of(const at::Device& device)
-{
-    PyObject* index = PyLong_FromLong(device.index());
-    PyObject* s = index ? PyObject_CallOneArg(g_raw_stream, index) : nullptr;
-    Py_XDECREF(index);
-    if (s == nullptr)
-        throw Raised();
-    const unsigned long long v = PyLong_AsUnsignedLongLong(s);
-    Py_DECREF(s);
-    if (PyErr_Occurred())
-        throw Raised();
-    return (Stream)(uintptr_t)v;
-}
-
-// the launch itself runs without the interpreter's lock
-template <typename F>
-void launch(const char* what, F&& call)
-{
-    int rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = call();
-    Py_END_ALLOW_THREADS
-    if (rc != 0)
-        refuse(std::string(what) + " failed: " + g_status(rc) + " (" + std::to_string(rc) + ")");
-}
-
-PyObject* given_or(PyObject* given, const at::Tensor& made)
-{
-    if (given == Py_None)
-        return THPVariable_Wrap(made);
-    Py_INCREF(given);
-    return given;
-}
-PyObject* none_or(PyObject* given, const at::Tensor& made)
-{
-    if (given == Py_None && !made.defined())
-        Py_RETURN_NONE;
-    return given_or(given, made);
-}
-
-template <typename F>
-PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& body)
-{
-    if (g_error == nullptr || got != want) {
-        PyErr_SetString(PyExc_TypeError, "binding called with wrong arguments or before init");
-        return nullptr;
-    }
-    try {
-        return body();
-    } catch (const Raised&) {
-    } catch (const Refused& e) {
-        PyErr_SetString(g_error, e.what());
-    } catch (const std::exception& e) {
-        PyErr_SetString(g_error, e.what());
-    } catch (...) {
-        PyErr_SetString(g_error, "unknown C++ exception");
-    }
-    return nullptr;
-}
 
 // logits, topk, score, bias, num_groups, topk_groups, group_top, renormalize,
 // scale, num_tokens, topk_ids, topk_weights
@@ -448,23 +261,22 @@ PyObject* gemm_epilogue(PyObject*, PyObject* const* a, Py_ssize_t n)
 }
 
 // error, raw_stream, addresses of w4a8_status_string, w4a8_moe_route,
-// w4a8_norm_residual, w4a8_gemm_epilogue
+// w4a8_norm_residual, w4a8_gemm_epilogue, then those of binding_attn.cpp
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    if (n != 6) {
-        PyErr_SetString(PyExc_TypeError, "init takes 6 arguments");
+    if (n != 6 + kAttnExports) {
+        PyErr_SetString(PyExc_TypeError, "init takes 10 arguments");
         return nullptr;
     }
-    uintptr_t p[4];
-    for (int i = 0; i < 4; ++i) {
-        p[i] = (uintptr_t)PyLong_AsUnsignedLongLong(a[2 + i]);
-        if (PyErr_Occurred())
-            return nullptr;
+    try {
+        g_status = (StatusFn)address(a[2]);
+        g_route = (RouteFn)address(a[3]);
+        g_norm = (NormFn)address(a[4]);
+        g_gemm = (GemmFn)address(a[5]);
+        attn_init(a + 6);
+    } catch (const Raised&) {
+        return nullptr;
     }
-    g_status = (StatusFn)p[0];
-    g_route = (RouteFn)p[1];
-    g_norm = (NormFn)p[2];
-    g_gemm = (GemmFn)p[3];
     Py_INCREF(a[0]);
     Py_INCREF(a[1]);
     Py_XDECREF(g_error);
@@ -479,6 +291,10 @@ PyMethodDef g_methods[] = {
     {"moe_route", (PyCFunction)(void (*)())moe_route, METH_FASTCALL, nullptr},
     {"norm_residual", (PyCFunction)(void (*)())norm_residual, METH_FASTCALL, nullptr},
     {"gemm_epilogue", (PyCFunction)(void (*)())gemm_epilogue, METH_FASTCALL, nullptr},
+    {"gemm_fp8", (PyCFunction)(void (*)())gemm_fp8, METH_FASTCALL, nullptr},
+    {"rope", (PyCFunction)(void (*)())rope, METH_FASTCALL, nullptr},
+    {"kv_append", (PyCFunction)(void (*)())kv_append, METH_FASTCALL, nullptr},
+    {"attn_decode", (PyCFunction)(void (*)())attn_decode, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1,5 +1,6 @@
-// dense_common.hpp -- what the kernels of w4a8_gemm_epilogue share: the int4
-// decode and the epilogue of four consecutive outputs.
+// dense_common.hpp -- what the kernels of w4a8_gemm_epilogue and w4a8_gemm_fp8
+// share: the epilogue of four consecutive outputs and of a wave's tile; and the
+// int4 decode.
 #pragma once
 
 #include "w4a8.h"
@@ -154,6 +155,52 @@ __device__ __forceinline__ void epilogue4(const DenseArgs& a, int64_t m, int64_t
         if (a.residual != nullptr)
             o[i] += bf16_to_f32(a.residual[m * a.ldr + n0 + i]);
         a.out[m * a.ldo + n0 + i] = (uint16_t)f32x2_to_bf16x2(o[i], 0.0f);
+    }
+}
+
+// Epilogue of a wave that holds 16 SL rows of 64 weight rows, acc[slice][fragment]
+// four columns 16 f + 4 (lane / 16) of row 16 slice + lane % 16: the wave lays 64 of
+// its rows at a time into its own part of LDS and takes them out row by row, so
+// that the stores of a row are one contiguous piece and the epilogue's code
+// stands here once.  `first_row`: the wave's first row in the tile of `rows` rows
+// that begins at row m0; n_wave: its first output column (with SwiGLU 32 gate
+// rows, then their 32 up rows).
+constexpr int kTileLdsStride = 68;  // floats; 64 columns and a pad against bank conflicts
+constexpr int kTileWaveLds = 64 * kTileLdsStride * 4;
+template <int SL>
+__device__ __forceinline__ void store_tile(const DenseArgs& d, const float (&acc)[SL][4][4], float* mine, int lane,
+                                           int rows, int first_row, int64_t m0, int64_t n_wave)
+{
+    const int q = lane >> 4, c16 = lane & 15;
+    const bool glu = d.act == W4A8_ACT_SWIGLU;
+    const int cols = glu ? 8 : 16;  // float4 columns of outputs per wave
+    const int c4 = lane & (cols - 1);
+    const int64_t n0 = n_wave + 4 * c4;
+#pragma unroll
+    for (int p = 0; p < SL / 4; ++p) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const float* v = acc[4 * p + s][f];
+                *(float4*)(mine + (16 * s + c16) * kTileLdsStride + 16 * f + 4 * q) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        __builtin_amdgcn_wave_barrier();  // one wave: LDS operations stay in order
+        const int first = first_row + 64 * p;
+#pragma unroll 1
+        for (int r = lane / cols; r < 64; r += 64 / cols) {
+            if (first + r >= rows)
+                break;
+            const float4 y = *(const float4*)(mine + r * kTileLdsStride + 4 * c4);
+            const float yv[4] = {y.x, y.y, y.z, y.w};
+            float uv[4] = {0, 0, 0, 0};
+            if (glu) {
+                const float4 u = *(const float4*)(mine + r * kTileLdsStride + 32 + 4 * c4);
+                uv[0] = u.x, uv[1] = u.y, uv[2] = u.z, uv[3] = u.w;
+            }
+            epilogue4(d, m0 + first + r, n0, yv, uv, load_epilogue4(d, m0 + first + r, n0));
+        }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 

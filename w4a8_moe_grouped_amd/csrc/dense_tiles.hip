@@ -140,8 +140,7 @@ struct Tile {
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int kA = 0, kW = kBM * kGroup, kSw = kW + kBN * kGroup, kSa = kSw + kBN * 4;
     static constexpr int kStage = kSa + kBM * 4;
-    static constexpr int kEpiStride = 68;  // floats; 64 columns and a pad against bank conflicts
-    static constexpr int kEpiWave = 64 * kEpiStride * 4;
+    static constexpr int kEpiWave = kTileWaveLds;
     static constexpr int kLds = 2 * kStage > WM * WN * kEpiWave ? 2 * kStage : WM * WN * kEpiWave;
     static_assert(kBM % kUnit == 0 && kBN % kUnit == 0 && SL % 4 == 0 && kLds <= 160 * 1024, "tile");
 };
@@ -296,41 +295,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_tile_kernel(const TileA
             __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);      // one promotion
         }
     }
-    // Epilogue: each wave lays 64 of its rows at a time into its own part of
-    // LDS and takes them out row by row, so that the stores of a row are one
-    // contiguous piece and the epilogue's code stands here once.
     barrier();  // the last stage has been read by everyone
-    const bool glu = d.act == W4A8_ACT_SWIGLU;
-    float* const mine = (float*)(smem + wave * L::kEpiWave);
-    const int cols = glu ? 8 : 16;  // float4 columns of outputs per wave
-    const int c4 = lane & (cols - 1);
-    const int64_t n0 = glu ? (int64_t)tn * (L::kBN / 2) + 32 * wn + 4 * c4 : (int64_t)tn * L::kBN + 64 * wn + 4 * c4;
-#pragma unroll
-    for (int p = 0; p < SL / 4; ++p) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const float* v = acc[4 * p + s][f];
-                *(float4*)(mine + (16 * s + c16) * L::kEpiStride + 16 * f + 4 * q) = make_float4(v[0], v[1], v[2], v[3]);
-            }
-        __builtin_amdgcn_wave_barrier();  // one wave: LDS operations stay in order
-        const int first = 16 * SL * wm + 64 * p;
-#pragma unroll 1
-        for (int r = lane / cols; r < 64; r += 64 / cols) {
-            if (first + r >= rows)
-                break;
-            const float4 y = *(const float4*)(mine + r * L::kEpiStride + 4 * c4);
-            const float yv[4] = {y.x, y.y, y.z, y.w};
-            float uv[4] = {0, 0, 0, 0};
-            if (glu) {
-                const float4 u = *(const float4*)(mine + r * L::kEpiStride + 32 + 4 * c4);
-                uv[0] = u.x, uv[1] = u.y, uv[2] = u.z, uv[3] = u.w;
-            }
-            epilogue4(d, m0 + first + r, n0, yv, uv, load_epilogue4(d, m0 + first + r, n0));
-        }
-        __builtin_amdgcn_wave_barrier();
-    }
+    store_tile<SL>(d, acc, (float*)(smem + wave * L::kEpiWave), lane, rows, 16 * SL * wm, m0,
+                   d.act == W4A8_ACT_SWIGLU ? (int64_t)tn * (L::kBN / 2) + 32 * wn : (int64_t)tn * L::kBN + 64 * wn);
 }
 
 namespace {

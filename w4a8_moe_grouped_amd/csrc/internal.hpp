@@ -270,4 +270,68 @@ size_t dense_tiles_workspace(int64_t M, int64_t K, int64_t N, int act);
 bool dense_tiles_fit(int64_t M, int64_t K, int64_t N, int act);
 hipError_t launch_dense_tiles(const DenseArgs& a, void* ws, hipStream_t s);
 
+// ---- dense linear on block-scaled fp8 weights (gemm_fp8.hip) ----
+// DenseArgs with w [R, K] e4m3 codes and sw [ceil(R/128), K/128]
+size_t gemm_fp8_workspace(int64_t M, int64_t K, int64_t N, int act);
+bool gemm_fp8_fits(int64_t M, int64_t K, int64_t N, int act);
+hipError_t launch_gemm_fp8(const DenseArgs& d, void* ws, hipStream_t s);
+
+// ---- rotary positions and the paged cache's append (rope.hip) ----
+struct Rows {  // [T, heads, D]
+    const void* p;
+    int64_t ts, hs;  // token and head stride, elements
+};
+struct CacheRows {  // one side of the paged cache
+    void* p;
+    int64_t ps, ts, hs;  // page, token and head stride, elements
+    float* scales;       // [pages, kv heads, page size], e4m3 only
+};
+struct RopeArgs {
+    Rows q, k, v;
+    void* q_out;
+    int64_t qo_ts, qo_hs;
+    int type, cache_type;  // W4A8_TYPE_*
+    int64_t T;
+    int32_t q_heads, kv_heads;  // kv_heads 0: no cache
+    int32_t D, R;
+    int interleaved;
+    float magnitude;
+    const int32_t* positions;
+    const double* frequencies;
+    CacheRows kc, vc;
+    const int64_t* slots;
+    int64_t num_slots;
+    int32_t page_size;
+};
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+bool rope_fits(const RopeArgs& a);
+struct FrequencyArgs {
+    int32_t R;
+    int scaling;
+    double base, factor, lo, hi;
+};
+hipError_t launch_rope_frequencies(const FrequencyArgs& a, double* out, hipStream_t s);
+
+// ---- attention of one token over the paged cache (attn_decode.hip) ----
+struct AttnArgs {
+    const void* q;
+    int64_t q_bs, q_hs;
+    int q_type, cache_type;
+    int32_t B, q_heads, kv_heads, D;
+    CacheRows kc, vc;
+    int64_t num_pages;
+    int32_t page_size;
+    const int32_t* table;
+    int64_t ld_table;
+    int32_t max_pages;
+    const int32_t* lens;
+    float scale;
+    int64_t window;  // 0: none
+    void* out;
+    int64_t o_bs, o_hs;
+    float* lse;  // [B, q_heads] or null
+};
+size_t attn_decode_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_len);
+hipError_t launch_attn_decode(const AttnArgs& a, void* ws, hipStream_t s);
+
 } // namespace w4a8

@@ -25,7 +25,8 @@ EXPORTS = ("w4a8_version", "w4a8_status_string", "w4a8_quantize_act", "w4a8_gemm
            "w4a8_fused_moe_prepacked", "w4a8_prepack_weights_fp4", "w4a8_fused_moe_fp4_prepacked",
            "w4a8_prepack_weights_bf16_scales", "w4a8_fused_moe_prepacked_static",
            "w4a8_fused_moe_recipe", "w4a8_fused_moe_prepacked_noalloc", "w4a8_fused_moe_bounded",
-           "w4a8_fused_moe_persistent", "w4a8_moe_route", "w4a8_norm_residual", "w4a8_gemm_epilogue")
+           "w4a8_fused_moe_persistent", "w4a8_moe_route", "w4a8_norm_residual", "w4a8_gemm_epilogue",
+           "w4a8_gemm_fp8", "w4a8_rope_frequencies", "w4a8_rope", "w4a8_kv_append", "w4a8_attn_decode")
 
 _lock = threading.Lock()
 _lib = None
@@ -33,6 +34,15 @@ _lib = None
 
 class W4A8Error(RuntimeError):
     pass
+
+
+class KVCache(ctypes.Structure):
+    """w4a8_kv_cache of w4a8.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("type", ctypes.c_int)] + \
+        [(n, ctypes.c_int64) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "k_page_stride",
+                                       "k_token_stride", "k_head_stride", "v_page_stride", "v_token_stride",
+                                       "v_head_stride")]
 
 
 def load(path: Optional[str] = None) -> ctypes.CDLL:
@@ -104,6 +114,19 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         L.w4a8_gemm_epilogue.restype = ci
         L.w4a8_gemm_epilogue.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, ci, ci, vp, i64, vp, i64,
                                          vp, sz, vp]
+        f64, cache = ctypes.c_double, ctypes.POINTER(KVCache)
+        L.w4a8_gemm_fp8.restype = ci
+        L.w4a8_gemm_fp8.argtypes = L.w4a8_gemm_epilogue.argtypes
+        L.w4a8_rope_frequencies.restype = ci
+        L.w4a8_rope_frequencies.argtypes = [i64, f64, ci, f64, f64, f64, f64, vp, vp]
+        L.w4a8_rope.restype = ci
+        L.w4a8_rope.argtypes = [vp, ci, i64, i64, i64, i64, i64, vp, vp, i64, ci, f32, vp, i64, i64, vp]
+        L.w4a8_kv_append.restype = ci
+        L.w4a8_kv_append.argtypes = [vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, ci, i64, vp, vp, vp, i64, ci,
+                                     f32, cache, vp, i64, i64, vp]
+        L.w4a8_attn_decode.restype = ci
+        L.w4a8_attn_decode.argtypes = [vp, ci, i64, i64, i64, i64, cache, vp, i64, i64, vp, f32, i64, vp, i64, i64,
+                                       vp, vp, sz, vp]
         if path is None:
             _lib = L
         return L
@@ -483,8 +506,8 @@ _native = None
 
 
 def _binding():
-    """The native half of the calls below (csrc/binding.cpp), built beside
-    libw4a8.so."""
+    """The native half of the calls below (csrc/binding.cpp, binding_attn.cpp),
+    built beside libw4a8.so."""
     global _native
     if _native is None:
         L = load()
@@ -494,7 +517,8 @@ def _binding():
             raise W4A8Error("_binding.so not built (run python -m w4a8_moe_grouped_amd.build): %s" % e)
         native.init(W4A8Error, torch._C._cuda_getCurrentRawStream,
                     *[ctypes.cast(f, ctypes.c_void_p).value for f in (
-                        L.w4a8_status_string, L.w4a8_moe_route, L.w4a8_norm_residual, L.w4a8_gemm_epilogue)])
+                        L.w4a8_status_string, L.w4a8_moe_route, L.w4a8_norm_residual, L.w4a8_gemm_epilogue,
+                        L.w4a8_gemm_fp8, L.w4a8_rope, L.w4a8_kv_append, L.w4a8_attn_decode)])
         _native = native
     return _native
 
@@ -555,6 +579,106 @@ def gemm_epilogue(a_q: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
     if act is None:
         raise W4A8Error("activation must be one of %s" % (tuple(ACTIVATIONS),))
     return (_native or _binding()).gemm_epilogue(a_q, a_scales, w, w_scales, bias, act, residual, out, workspace)
+
+
+# ---- the attention half of a served block ----------------------------------------------
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def gemm_fp8_workspace_bytes(M: int, K: int, N: int, activation: str = "none") -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().w4a8_gemm_fp8(None, None, M, K, None, None, N, None, 0, ACTIVATIONS[activation], None, N, None,
+                                N, None, ctypes.byref(n), None), "w4a8_gemm_fp8(query)")
+    return n.value
+
+
+def gemm_fp8(a_q: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+             bias: Optional[torch.Tensor] = None, activation: str = "none",
+             residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None):
+    """w4a8_gemm_fp8: bf16 [M, N] = act(A * W^T + bias) + residual on e4m3
+    weights.  a_q, a_scales: codes (uint8 or float8_e4m3fn) and scales as
+    quantize_act makes them; w: codes [rows, K]; w_scales: fp32
+    [ceil(rows/128), K/128], one for each 128 x 128 block; rows is N, or 2N with
+    activation "swiglu" (gate rows, then up rows, N a multiple of 128).  The
+    rest as for gemm_epilogue."""
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise W4A8Error("activation must be one of %s" % (tuple(ACTIVATIONS),))
+    return (_native or _binding()).gemm_fp8(a_q, a_scales, w, w_scales, bias, act, residual, out, workspace)
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device="cuda") -> torch.Tensor:
+    """w4a8_rope_frequencies: the angle per position of each pair, fp64
+    [rotary_dim / 2], for rope and kv_append.  scaling: "none", "linear", "ntk"
+    or "yarn" (with original_length, beta_fast and beta_slow)."""
+    kind = ROPE_SCALINGS.get(scaling)
+    if kind is None:
+        raise W4A8Error("scaling must be one of %s" % (tuple(ROPE_SCALINGS),))
+    f = torch.empty(max(int(rotary_dim), 0) // 2, dtype=torch.float64, device=device)
+    _need_cuda(f)
+    with torch.cuda.device(f.device):
+        _check(load().w4a8_rope_frequencies(rotary_dim, base, kind, factor, original_length, beta_fast, beta_slow,
+                                            _ptr(f), _stream(f.device)), "w4a8_rope_frequencies")
+    return f
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, interleaved: bool = False,
+         magnitude: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """w4a8_rope: x [T, heads, D] (fp32, bf16 or fp16; any token and head
+    stride that is a multiple of 8) with the first 2 * len(frequencies)
+    elements of each head rotated by positions (int32 [T]) times frequencies
+    (fp64, from rope_frequencies); interleaved: pairs side by side instead of
+    halves.  magnitude multiplies the rotated elements.  out may be x."""
+    return (_native or _binding()).rope(x, positions, frequencies, interleaved, magnitude, out)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor,
+              k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None, frequencies: Optional[torch.Tensor] = None,
+              interleaved: bool = False, magnitude: float = 1.0, q: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """w4a8_kv_append: writes k and v ([T, kv_heads, D], bf16 or fp16) into
+    the paged cache at slots (int64 [T]: page * page_size + place; a slot
+    outside the cache, such as -1, is not written), k rotated as by rope, and
+    returns q ([T, q_heads, D]) rotated, or None without q.  Without positions
+    and frequencies nothing is rotated.
+    k_cache, v_cache: [pages, page_size, kv_heads, D] of k's type, or uint8 (or
+    float8_e4m3fn) codes with k_scales, v_scales fp32 [pages, kv_heads,
+    page_size]; any strides that are multiples of 8, unit in D, so a cache laid
+    out [pages, kv_heads, page_size, D] is passed as its transpose(1, 2)."""
+    return (_native or _binding()).kv_append(k, v, k_cache, v_cache, slots, k_scales, v_scales, positions,
+                                             frequencies, interleaved, magnitude, q, q_out)
+
+
+def attn_decode_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: int, max_pages: int,
+                                page_size: int) -> int:
+    n = ctypes.c_size_t(0)
+    c = KVCache(kv_heads=kv_heads, head_dim=head_dim, page_size=page_size)
+    _check(load().w4a8_attn_decode(None, 1, B, q_heads, 0, 0, ctypes.byref(c), None, max_pages, max_pages, None, 1.0,
+                                   0, None, 0, 0, None, None, ctypes.byref(n), None), "w4a8_attn_decode(query)")
+    return n.value
+
+
+def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                seq_lens: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
+                v_scales: Optional[torch.Tensor] = None, scale: Optional[float] = None, window: int = 0,
+                return_lse: bool = False, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None):
+    """w4a8_attn_decode: attention of one token of each sequence, q [B,
+    q_heads, D], over the paged cache (as kv_append has it, the new token
+    appended already).  page_table: int32 [B, max_pages], entries outside the
+    cache hold nothing; seq_lens: int32 [B], the new token included; scale: 1 /
+    sqrt(D) if not given; window: the last tokens that are seen, 0 for all.
+    Returns (out of q's shape and type, lse fp32 [B, q_heads] or None): a
+    sequence without tokens has 0 and -inf.  q is of the cache's type, bf16 with
+    codes.  workspace: a contiguous tensor of at least
+    attn_decode_workspace_bytes bytes; allocated if not given."""
+    return (_native or _binding()).attn_decode(q, k_cache, v_cache, page_table, seq_lens, k_scales, v_scales, scale,
+                                               window, return_lse, out, lse, workspace)
 
 
 STAGES = ("align", "quant", "gate_up", "down", "combine")
