@@ -434,6 +434,16 @@ def test_attn_decode_batches(dev, kind, lens):
     check_attn(make_batch(dev, lens, 8, 2, 64, kind, 64))
 
 
+@pytest.mark.parametrize("kind", [BF16, FP16, "fp8"])
+@pytest.mark.parametrize("D", [64, 128, 256, 72])
+@pytest.mark.parametrize("page", [16, 5])
+def test_attn_decode_short_sequences_in_wide_tables(dev, kind, D, page):
+    """Tables for far more tokens than there are: what little there is, is cut."""
+    for lens in (LENS, [1], [0, 0], [129] * 70, [5, 900, 1, 0, 0, 2000, 64]):
+        check_attn(make_batch(dev, lens, 8, 2, D, kind, page, extra=3000))
+        check_attn(make_batch(dev, lens, 8, 2, D, kind, page, extra=3000), window=70)
+
+
 def test_attn_decode_one_page_each(dev):
     """Tables that hold no more than one unit are not cut."""
     for page in (16, 64, 128, 9):
@@ -517,9 +527,9 @@ def test_attn_decode_strides_outputs_and_workspace(dev):
     wide = torch.randn(3, 12, 96, generator=gen(dev, 8), device=dev).to(BF16)
     wide[:, 2:10, :80] = d["q"]
     d["q"] = wide[:, 2:10, :80]
-    big = torch.zeros(3, 40, dtype=torch.int32, device=dev) - 1
+    big = torch.zeros(3, 2010, dtype=torch.int32, device=dev) - 1  # wide enough for a workspace
     big[:, :d["page_table"].shape[1]] = d["page_table"]
-    d["page_table"] = big[:, :d["page_table"].shape[1]]
+    d["page_table"] = big[:, :2000]
     need = w4.attn_decode_workspace_bytes(3, 8, 2, 80, d["page_table"].shape[1], 16)
     out = torch.full((3, 9, 80), 7.0, dtype=BF16, device=dev)
     lse = torch.empty(3, 8, device=dev)

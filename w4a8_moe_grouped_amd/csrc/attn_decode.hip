@@ -32,10 +32,8 @@ namespace w4a8 {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kTile = 32;                // keys a wave takes at a time
-constexpr int kUnit = kTile * kWaves;    // keys a workgroup takes at a time
+constexpr int kJoinWaves = 4;
+constexpr int kUnit = 128;               // keys: what work is counted and cut in
 constexpr int kHeads = 16;               // columns of a product
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
@@ -52,7 +50,7 @@ struct Plan {
     int32_t page_shift;
     int64_t* header;        // total units, workgroups in use; then the first unit of each sequence
     float* part_o;          // [2 workgroups][16][D]
-    float2* part_ml;        // [2 workgroups][16]: reference, sum
+    float2* part_ml;        // [2 workgroups][16]: maximum, sum
 };
 
 __device__ __forceinline__ int page_of(const Plan& p, int key)
@@ -60,10 +58,9 @@ __device__ __forceinline__ int page_of(const Plan& p, int key)
     return (int)(__umulhi((uint32_t)key << 1, p.page_mul) >> p.page_shift);
 }
 
-// keys [start, end) that sequence b sees
-__device__ __forceinline__ void span_of(const AttnArgs& a, int b, int& start, int& end)
+// keys [start, end) that a sequence of this length sees
+__device__ __forceinline__ void span_of(const AttnArgs& a, int64_t len, int& start, int& end)
 {
-    const int64_t len = a.lens[b];
     const int64_t table = (int64_t)a.max_pages * a.page_size;
     end = (int)min(max(len, (int64_t)0), table);
     start = a.window > 0 ? (int)min(max(len - a.window, (int64_t)0), table) : 0;
@@ -73,12 +70,46 @@ __device__ __forceinline__ int units_of(int start, int end)
     return start < end ? (end + kUnit - 1) / kUnit - start / kUnit : 0;
 }
 
-// a value that is the same in all lanes, in scalar registers
-__device__ __forceinline__ int64_t uniform(int64_t v)
+// lane l's value, in scalar registers
+__device__ __forceinline__ int64_t uniform(int64_t v, int l)
 {
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, l);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)v >> 32), l);
     return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// floor(x / y), 0 <= x < 2^52, 0 < y < 2^31
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)
+{
+    int64_t q = (int64_t)((double)x / (double)y);
+    const int64_t r = x - q * y;
+    q += r >= y ? 1 : 0;
+    return q - (r < 0 ? 1 : 0);
+}
+
+// the first unit of workgroup w of n, which share `total` units: the first
+// total % n of them have one more
+__device__ __forceinline__ int64_t begin_of(int64_t total, int n, int w)
+{
+    const int64_t each = quotient(total, n), more = total - each * n;
+    return each * w + min((int64_t)w, more);
+}
+// the workgroup that holds unit u
+__device__ __forceinline__ int holder_of(int64_t total, int n, int64_t u)
+{
+    const int64_t each = quotient(total, n), more = total - each * n, big = (each + 1) * more;
+    return (int)(u < big ? quotient(u, each + 1) : more + quotient(u - big, max(each, (int64_t)1)));
+}
+
+// inclusive sums over the lanes
+__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t x = __shfl_up(v, o, 64);
+        v += lane >= o ? x : 0;
+    }
+    return v;
 }
 
 __device__ __forceinline__ float exp2_(float x)
@@ -86,7 +117,10 @@ __device__ __forceinline__ float exp2_(float x)
     return __builtin_amdgcn_exp2f(x);
 }
 
-// the operand types of one kind of cache
+// The operand types of one kind of cache.  split: weights as a value cut to the
+// type and what the cut left, both above zero (zero times an infinite value
+// would be NaN).  fp16 holds the weights times 2^kShift: they stay below 2^(8 + kShift), and what is
+// added to a small one, below 2^-24, is 2^-31 of the reference.
 template <int CT>
 struct Kind;
 template <>
@@ -96,6 +130,14 @@ struct Kind<W4A8_TYPE_BF16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
     }
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return f32x2_to_bf16x2(a, b); }
+    static constexpr float kShift = 0.0f;
+    static __device__ __forceinline__ void split(float a, float b, int& hi, int& lo)
+    {
+        hi = (int)__builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+        a -= __uint_as_float(__float_as_uint(a) & 0xFFFF0000u);
+        b -= __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
+        lo = (int)pack(fmaxf(a, 0x1p-100f), fmaxf(b, 0x1p-100f));
+    }
 };
 template <>
 struct Kind<W4A8_TYPE_FP16> {
@@ -106,6 +148,13 @@ struct Kind<W4A8_TYPE_FP16> {
     static __device__ __forceinline__ uint32_t pack(float a, float b)
     {
         return __builtin_bit_cast(uint32_t, v2h{(_Float16)a, (_Float16)b});
+    }
+    static constexpr float kShift = 7.0f;
+    static __device__ __forceinline__ void split(float a, float b, int& hi, int& lo)
+    {
+        const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
+        hi = __builtin_bit_cast(int, h);
+        lo = (int)pack(fmaxf(a - (float)h[0], 0x1p-24f), fmaxf(b - (float)h[1], 0x1p-24f));
     }
 };
 template <>
@@ -118,6 +167,23 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16(uint32_t d)
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, HIGH));
 }
 
+// tiles of 32 keys that a wave takes at a time: 16 to 32 KB of cache
+constexpr int tiles_of(int ct, int dp, bool cut)
+{
+    return dp == 256 ? 1 : ct == W4A8_TYPE_E4M3 || dp == 64 || !cut ? 2 : 1;
+}
+// waves of a workgroup
+constexpr int waves_of(int dp, bool cut)
+{
+    return cut || dp == 256 ? 4 : 8;
+}
+
+template <typename T>
+__device__ __forceinline__ T load(const char* p)
+{
+    return *(const T*)p;
+}
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 template <int BYTES>
 struct Chunk;
 template <>
@@ -126,7 +192,7 @@ struct Chunk<4> {
 };
 template <>
 struct Chunk<8> {
-    typedef uint2 T;
+    typedef v2u T;
 };
 template <>
 struct Chunk<16> {
@@ -138,9 +204,12 @@ struct Chunk<16> {
 // CT: type of the cache.  DP: D rounded up to 64, 128 or 256.  PAD: D < DP (or
 // rows of codes that are not 16-byte aligned): chunks past D are not read.
 // RUNS: pages hold whole runs of 8 keys, so a lane's 8 keys share a page.
-template <int CT, int DP, bool PAD, bool RUNS>
-__global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_decode_kernel(const Plan p)
+template <int CT, int DP, bool PAD, bool RUNS, bool CUT>
+__global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void attn_decode_kernel(const Plan p)
 {
+    constexpr int kWaves = waves_of(DP, CUT);
+    constexpr int NT = tiles_of(CT, DP, CUT);  // tiles of 32 keys that a wave takes at a time
+    constexpr int kTile = 32 * NT;
     using K = Kind<CT>;
     constexpr bool FP8 = CT == W4A8_TYPE_E4M3;
     constexpr int kElem = FP8 ? 1 : 2;
@@ -152,86 +221,72 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_decode_kerne
     using VChunk = typename Chunk<kPer * kElem>::T;
     constexpr int kVWords = kPer * kElem / 4;
 
+    const int me = (int)blockIdx.x;
     const AttnArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     __shared__ float sh_o[kWaves][kOut * 4][64];
     __shared__ float2 sh_ml[kWaves][kHeads];
-    __shared__ int64_t sh_sum[kThreads];
-    __shared__ int64_t sh_at[2];  // sequence, its first unit
-
     // where this workgroup's work begins
     int64_t u = 0, u_end = 0;  // in units of the whole batch
     int b = 0;
     int64_t b_first = 0;       // first unit of sequence b
-    if (p.cut) {
-        // thread i sums the units of an equal part of the sequences
-        const int per = (a.B + kThreads - 1) / kThreads;
-        const int first = tid * per, last = min(first + per, a.B);
-        int64_t mine = 0;
-        for (int i = first; i < last; ++i) {
+    const int lens0 = CUT && lane < a.B ? a.lens[lane] : 0;  // of the first 64
+    if (CUT) {
+        // every wave for itself, 64 sequences at a time: no barrier, and one load for a batch of up to 64
+        auto units_at = [&](int len) {
             int s, e;
-            span_of(a, i, s, e);
-            mine += units_of(s, e);
-        }
-        mine *= p.items;
-        sh_sum[tid] = mine;
-        __syncthreads();
-        for (int o = 1; o < kThreads; o <<= 1) {
-            const int64_t v = tid >= o ? sh_sum[tid - o] : 0;
-            __syncthreads();
-            sh_sum[tid] += v;
-            __syncthreads();
-        }
-        const int64_t total = uniform(sh_sum[kThreads - 1]);
+            span_of(a, len, s, e);
+            return (int64_t)units_of(s, e);
+        };
+        auto len_at = [&](int i) { return i < a.B ? a.lens[i] : 0; };
+        const int64_t first = units_at(lens0);
+        int64_t total = first;
+        for (int at = 64; at < a.B; at += 64)
+            total += units_at(len_at(at + lane));
+        total = uniform(wave_scan(total, lane), 63) * p.items;
         const int in_use = (int)min((int64_t)p.workgroups, total);
-        const int64_t before = sh_sum[tid] - mine;
-        if (blockIdx.x == 0) {  // for the join
-            if (tid == 0) {
+        if (blockIdx.x == 0 && wave == 0) {  // for the join
+            if (lane == 0) {
                 p.header[0] = total;
                 p.header[1] = in_use;
             }
-            int64_t at = before;
-            for (int i = first; i < last; ++i) {
-                p.header[2 + i] = at;
-                int s, e;
-                span_of(a, i, s, e);
-                at += (int64_t)units_of(s, e) * p.items;
+            int64_t before = 0;
+            for (int at = 0; at < a.B; at += 64) {
+                const int64_t n = at ? units_at(len_at(at + lane)) : first, sum = wave_scan(n, lane);
+                if (at + lane < a.B)
+                    p.header[3 + at + lane] = (before + sum) * p.items;
+                if (at + lane == 0)
+                    p.header[2] = 0;
+                before += uniform(sum, 63);
             }
-            if (last == a.B && first < last)
-                p.header[2 + a.B] = at;
         }
-        if ((int)blockIdx.x >= in_use)
+        if (me >= in_use)
             return;
-        u = total * (int)blockIdx.x / in_use;
-        u_end = total * ((int)blockIdx.x + 1) / in_use;
-        if (before <= u && u < before + mine) {
-            int64_t at = before;
-            for (int i = first; i < last; ++i) {
-                int s, e;
-                span_of(a, i, s, e);
-                const int64_t n = (int64_t)units_of(s, e) * p.items;
-                if (u < at + n) {
-                    sh_at[0] = i;
-                    sh_at[1] = at;
-                    break;
-                }
-                at += n;
+        u = begin_of(total, in_use, me);
+        u_end = begin_of(total, in_use, me + 1);
+        int64_t before = 0;
+        for (int at = 0; at < a.B; at += 64) {
+            const int64_t n = at ? units_at(len_at(at + lane)) : first, sum = wave_scan(n, lane);
+            const uint64_t behind = __ballot((before + sum) * p.items > u);
+            if (behind != 0) {
+                const int l = __builtin_ctzll(behind);
+                b = at + l;
+                b_first = (before + uniform(sum - n, l)) * p.items;
+                break;
             }
+            before += uniform(sum, 63);
         }
-        __syncthreads();
-        b = (int)uniform(sh_at[0]);
-        b_first = uniform(sh_at[1]);
     }
 
     const float c = a.scale * kLog2e;
     for (int segment = 0;; ++segment) {
         int start, end, item, unit0, unit1, units;
-        if (p.cut) {
+        if (CUT) {
             if (u >= u_end)
                 break;
-            span_of(a, b, start, end);
+            span_of(a, b < 64 ? __builtin_amdgcn_readlane(lens0, b) : a.lens[b], start, end);
             units = units_of(start, end);
             if (u >= b_first + (int64_t)units * p.items) {
                 b_first += (int64_t)units * p.items;
@@ -239,7 +294,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_decode_kerne
                 --segment;
                 continue;
             }
-            item = (int)((u - b_first) / units);
+            item = (int)quotient(u - b_first, units);
             unit0 = (int)(u - b_first - (int64_t)item * units);
             unit1 = (int)min((int64_t)units, unit0 + (u_end - u));
             u += unit1 - unit0;
@@ -248,14 +303,13 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_decode_kerne
                 break;
             b = (int)blockIdx.x / p.items;
             item = (int)blockIdx.x - b * p.items;
-            span_of(a, b, start, end);
+            span_of(a, a.lens[b], start, end);
             units = units_of(start, end);
             unit0 = 0;
             unit1 = units;
         }
         const int kv = item / p.blocks, head0 = kv * p.group + (item - kv * p.blocks) * kHeads;
         const int heads = min(kHeads, (kv + 1) * p.group - head0);
-        const int tile_base = start / kUnit * kWaves + wave;
         const int32_t* table = a.table + b * a.ld_table;
 
         // the queries: column c16, positions of d as the keys' loads give them
@@ -273,240 +327,291 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_decode_kerne
 #pragma unroll
         for (int i = 0; i < kOut; ++i)
             o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        float m = -__builtin_inff(), ref = 0.0f, l = 0.0f;
+        float m = -__builtin_inff(), ref = -K::kShift, l = 0.0f;
 
         const char* const kbase = (const char*)a.kc.p + kv * a.kc.hs * kElem;
         const char* const vbase = (const char*)a.vc.p + kv * a.vc.hs * kElem;
         const int64_t kts = a.kc.ts * kElem, kps = a.kc.ps * kElem, vts = a.vc.ts * kElem, vps = a.vc.ps * kElem;
 
-        v4i kreg[2][kKLoads];
-        VChunk vreg[8][kHalves];
-        float ksc[8], vsc[8];
-        uint32_t mask = 0;  // which of the lane's 8 keys 8g.. of the tile are there
+        v4i kreg[NT][2][kKLoads];
+        VChunk vreg[NT][8][kHalves];
+        float ksc[NT][8], vsc[NT][8];
+        uint32_t mask = 0;  // which of the lane's keys 32 n + 8 g + j of the tile are there, bit 8 n + j
+        constexpr uint32_t kAll = NT == 4 ? 0xFFFFFFFFu : (1u << (8 * NT & 31)) - 1;
 
-        // the page of the key `key`, or -1
-        auto lookup = [&](int key) {
-            if (key < start || key >= end)
+        // the page of key `key`, or of the run of keys from `key`; -1: nothing of it is seen
+        auto held = [&](int id) { return id >= 0 && id < a.num_pages ? id : -1; };
+        auto lookup = [&](int key, int run) {
+            if (key + run <= start || key >= end)
                 return -1;
-            const int id = table[page_of(p, key)];
-            return id >= 0 && id < a.num_pages ? id : -1;
+            return held(table[page_of(p, key)]);
         };
-        // the page of the run of 8 keys from `key`, or -1
-        auto lookup_run = [&](int key) {
-            if (key + 8 <= start || key >= end)
-                return -1;
-            const int id = table[page_of(p, key)];
-            return id >= 0 && id < a.num_pages ? id : -1;
-        };
-        auto load_k_row = [&](int t, const char* row) {
+        auto load_k_row = [&](int n, int t, const char* row) {
 #pragma unroll
             for (int i = 0; i < kKLoads; ++i) {
                 if (!FP8) {
                     const int d = 32 * i + 8 * g;
-                    kreg[t][i] = !PAD || d < a.D ? ldg16(row + 2 * d) : v4i{0, 0, 0, 0};
+                    kreg[n][t][i] = !PAD || d < a.D ? load<v4i>(row + 2 * d) : v4i{0, 0, 0, 0};
                 } else if (!PAD) {
-                    kreg[t][i] = ldg16(row + 64 * i + 16 * g);
+                    kreg[n][t][i] = load<v4i>(row + 64 * i + 16 * g);
                 } else {
                     const int d = 64 * i + 16 * g;
                     const uint2 x = d < a.D ? *(const uint2*)(row + d) : make_uint2(0, 0);
                     const uint2 y = d + 8 < a.D ? *(const uint2*)(row + d + 8) : make_uint2(0, 0);
-                    kreg[t][i] = v4i{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+                    kreg[n][t][i] = v4i{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
                 }
             }
         };
-        auto load_v_row = [&](int j, const char* row) {
+        auto load_v_row = [&](int n, int j, const char* row) {
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
                 const int d = 128 * h + kPer * c16;
                 if (!PAD || d < a.D)
-                    vreg[j][h] = *(const VChunk*)(row + d * kElem);
+                    vreg[n][j][h] = load<VChunk>(row + d * kElem);
                 else
-                    vreg[j][h] = VChunk{};
+                    vreg[n][j][h] = VChunk{};
             }
         };
-        const int krun = 8 * (c16 >> 2);  // this lane's key row in a tile is in the run of that key
-        auto load_k = [&](int tile, int idk) {
-            const int key0 = tile * kTile;
-            if (RUNS) {
-                const int key = key0 + krun;
-                const int off = idk >= 0 ? key - page_of(p, key) * a.page_size : 0;
-                const char* row = kbase + max(idk, 0) * kps + (off + (c16 & 3)) * kts;
-                load_k_row(0, row);
-                load_k_row(1, row + 4 * kts);
-            } else {
+        // a lane's key row of tile t of a pair is key krun + 4 t + c16 % 4; its run of values is from key 8 g
+        const int krun = 8 * (c16 >> 2), vrun = 8 * g;
+        struct Ids {
+            int k[NT], v[NT];
+        };
+        auto lookup_all = [&](int key0) {
+            Ids id;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int key = key0 + krun + 4 * t + (c16 & 3);
-                    const int id = lookup(key);
-                    const int off = id >= 0 ? key - page_of(p, key) * a.page_size : 0;
-                    load_k_row(t, kbase + max(id, 0) * kps + off * kts);
+            for (int n = 0; n < NT; ++n) {
+                id.k[n] = RUNS ? lookup(key0 + 32 * n + krun, 8) : -1;
+                id.v[n] = RUNS ? lookup(key0 + 32 * n + vrun, 8) : -1;
+            }
+            return id;
+        };
+        auto load_k = [&](int key0, const Ids& id) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (RUNS) {
+                    const int key = key0 + 32 * n + krun;
+                    const int off = id.k[n] >= 0 ? key - page_of(p, key) * a.page_size : 0;
+                    const char* row = kbase + max(id.k[n], 0) * kps + (off + (c16 & 3)) * kts;
+                    load_k_row(n, 0, row);
+                    load_k_row(n, 1, row + 4 * kts);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int key = key0 + 32 * n + krun + 4 * t + (c16 & 3);
+                        const int one = lookup(key, 1);
+                        const int off = one >= 0 ? key - page_of(p, key) * a.page_size : 0;
+                        load_k_row(n, t, kbase + max(one, 0) * kps + off * kts);
+                    }
                 }
             }
         };
-        auto load_v = [&](int tile, int idv) {
-            const int key = tile * kTile + 8 * g;
+        auto load_v = [&](int key0, const Ids& id) {
             mask = 0;
-            if (RUNS) {
-                const int off = idv >= 0 ? key - page_of(p, key) * a.page_size : 0;
-                const char* row = vbase + max(idv, 0) * vps + off * vts;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    load_v_row(j, row + j * vts);
-                if (idv >= 0) {
+            for (int n = 0; n < NT; ++n) {
+                const int key = key0 + 32 * n + vrun;
+                if (RUNS) {
+                    const int page = max(id.v[n], 0);
+                    const int off = id.v[n] >= 0 ? key - page_of(p, key) * a.page_size : 0;
+                    const char* row = vbase + page * vps + off * vts;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        load_v_row(n, j, row + j * vts);
                     const int lo = max(start - key, 0), hi = min(end - key, 8);
-                    mask = (0xFFu << lo) & (0xFFu >> (8 - hi)) & 0xFFu;
-                }
-                if (FP8) {
-                    const int64_t at = ((int64_t)max(idv, 0) * a.kv_heads + kv) * a.page_size + off;
-#pragma unroll
-                    for (int j = 0; j < 8; j += 4) {
-                        const float4 x = *(const float4*)(a.kc.scales + at + j), y = *(const float4*)(a.vc.scales + at + j);
-                        ksc[j] = x.x, ksc[j + 1] = x.y, ksc[j + 2] = x.z, ksc[j + 3] = x.w;
-                        vsc[j] = y.x, vsc[j + 1] = y.y, vsc[j + 2] = y.z, vsc[j + 3] = y.w;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int id = lookup(key + j);
-                    const int off = id >= 0 ? key + j - page_of(p, key + j) * a.page_size : 0;
-                    load_v_row(j, vbase + max(id, 0) * vps + off * vts);
+                    if (id.v[n] >= 0)
+                        mask |= ((0xFFu << lo) & (0xFFu >> (8 - hi)) & 0xFFu) << (8 * n);
                     if (FP8) {
-                        const int64_t at = ((int64_t)max(id, 0) * a.kv_heads + kv) * a.page_size + off;
-                        ksc[j] = a.kc.scales[at];
-                        vsc[j] = a.vc.scales[at];
+                        const int64_t at = ((int64_t)page * a.kv_heads + kv) * a.page_size + off;
+#pragma unroll
+                        for (int j = 0; j < 8; j += 4) {
+                            const float4 x = *(const float4*)(a.kc.scales + at + j), y = *(const float4*)(a.vc.scales + at + j);
+                            ksc[n][j] = x.x, ksc[n][j + 1] = x.y, ksc[n][j + 2] = x.z, ksc[n][j + 3] = x.w;
+                            vsc[n][j] = y.x, vsc[n][j + 1] = y.y, vsc[n][j + 2] = y.z, vsc[n][j + 3] = y.w;
+                        }
                     }
-                    mask |= (id >= 0 ? 1u : 0u) << j;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int one = lookup(key + j, 1);
+                        const int off = one >= 0 ? key + j - page_of(p, key + j) * a.page_size : 0;
+                        load_v_row(n, j, vbase + max(one, 0) * vps + off * vts);
+                        if (FP8) {
+                            const int64_t at = ((int64_t)max(one, 0) * a.kv_heads + kv) * a.page_size + off;
+                            ksc[n][j] = a.kc.scales[at];
+                            vsc[n][j] = a.vc.scales[at];
+                        }
+                        mask |= (one >= 0 ? 1u : 0u) << (8 * n + j);
+                    }
                 }
             }
         };
 
-        // this wave's tiles, those that hold a key that is seen
-        int tile = tile_base + unit0 * kWaves;
-        const int tile_end = min(tile_base - wave + unit1 * kWaves, (end + kTile - 1) / kTile);
-        while (tile < tile_end && (tile + 1) * kTile <= start)
-            tile += kWaves;
-        int idk = -1, idv = -1;
-        if (tile < tile_end) {
-            if (RUNS) {
-                idk = lookup_run(tile * kTile + krun);
-                idv = lookup_run(tile * kTile + 8 * g);
+        // the segment's keys, in tiles that the waves take in turn
+        constexpr int kStep = kTile * kWaves;
+        const int seg0 = (start / kUnit + unit0) * kUnit, seg1 = min((start / kUnit + unit1) * kUnit, end);
+        int key0 = seg0 + wave * kTile;
+        while (key0 < seg1 && key0 + kTile <= start)
+            key0 += kStep;
+        Ids ids;
+        if (!CUT && RUNS && a.window == 0) {
+            // the first tile's place is known without the length: its pages are
+            // looked up while the length is on its way
+            auto early = [&](int key) {
+                const int id = table[min(page_of(p, key), a.max_pages - 1)];
+                return key < end ? held(id) : -1;
+            };
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                ids.k[n] = early(wave * kTile + 32 * n + krun);
+                ids.v[n] = early(wave * kTile + 32 * n + vrun);
             }
-            load_k(tile, idk);
-            load_v(tile, idv);
-            if (RUNS && tile + kWaves < tile_end) {
-                idk = lookup_run((tile + kWaves) * kTile + krun);
-                idv = lookup_run((tile + kWaves) * kTile + 8 * g);
-            }
+        } else {
+            ids = lookup_all(key0 < seg1 ? key0 : end);
         }
-        for (; tile < tile_end; tile += kWaves) {
-            const bool more = tile + kWaves < tile_end;
-            v4f s[2] = {v4f{0.0f, 0.0f, 0.0f, 0.0f}, v4f{0.0f, 0.0f, 0.0f, 0.0f}};
+        if (key0 < seg1) {
+            load_k(key0, ids);
+            load_v(key0, ids);
+            if (RUNS && key0 + kStep < seg1)
+                ids = lookup_all(key0 + kStep);
+        }
+        for (; key0 < seg1; key0 += kStep) {
+            const bool more = key0 + kStep < seg1;
+            v4f s[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    s[n][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    v4i x;
-                    if (FP8) {
-                        const uint32_t d0 = (uint32_t)kreg[t][k >> 1][2 * (k & 1)], d1 = (uint32_t)kreg[t][k >> 1][2 * (k & 1) + 1];
-                        x = v4i{(int)fp8x2_to_bf16<false>(d0), (int)fp8x2_to_bf16<true>(d0), (int)fp8x2_to_bf16<false>(d1),
-                                (int)fp8x2_to_bf16<true>(d1)};
-                    } else {
-                        x = kreg[t][FP8 ? 0 : k];
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        v4i x;
+                        if (FP8) {
+                            const v4i& r = kreg[n][t][k >> 1];
+                            const uint32_t d0 = (uint32_t)r[2 * (k & 1)], d1 = (uint32_t)r[2 * (k & 1) + 1];
+                            x = v4i{(int)fp8x2_to_bf16<false>(d0), (int)fp8x2_to_bf16<true>(d0), (int)fp8x2_to_bf16<false>(d1),
+                                    (int)fp8x2_to_bf16<true>(d1)};
+                        } else {
+                            x = kreg[n][t][FP8 ? 0 : k];
+                        }
+                        s[n][t] = K::mfma(x, q[k], s[n][t]);
                     }
-                    s[t] = K::mfma(x, q[k], s[t]);
-                }
-            int idv_next = idv;
+            Ids next = ids;
             if (more) {
-                const int idk_now = idk;
-                if (RUNS && tile + 2 * kWaves < tile_end) {
-                    idk = lookup_run((tile + 2 * kWaves) * kTile + krun);
-                    idv_next = lookup_run((tile + 2 * kWaves) * kTile + 8 * g);
-                }
-                load_k(tile + kWaves, idk_now);
+                if (RUNS && key0 + 2 * kStep < seg1)
+                    next = lookup_all(key0 + 2 * kStep);
+                load_k(key0 + kStep, ids);
             }
             // scores in powers of two; those that are not there are -inf
-            float x[8];
+            float x[NT][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[j] = s[j >> 2][j & 3] * (FP8 ? c * ksc[j] : c);
-            const bool whole = __all(mask == 0xFFu);
-            if (!whole) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    x[j] = mask >> j & 1 ? x[j] : -__builtin_inff();
+                    x[n][j] = s[n][j >> 2][j & 3] * (FP8 ? c * ksc[n][j] : c);
+            const bool whole = __all(mask == kAll);
+            if (!whole) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[n][j] = mask >> (8 * n + j) & 1 ? x[n][j] : -__builtin_inff();
             }
-            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            float top = x[0][0];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = fmaxf(top, x[n][j]);
             if (__any(top > m + 8.0f)) {
                 top = fmaxf(top, __shfl_xor(top, 16, 64));
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const float next = fmaxf(m, top);
-                const float next_ref = next == -__builtin_inff() ? 0.0f : next;
+                const float high = fmaxf(m, top);
+                const float next_ref = high == -__builtin_inff() ? 0.0f : high;
                 const float f = exp2_(m - next_ref);
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < kOut; ++i)
                     o[i] *= f;
-                m = next;
-                ref = next_ref;
-            }
-            float w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                w[j] = exp2_(x[j] - ref);
-                l += w[j];
-                if (FP8)
-                    w[j] *= vsc[j];
+                m = high;
+                ref = next_ref - K::kShift;
             }
             if (!whole) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool in = mask >> j & 1;
-                    w[j] = in ? w[j] : 0.0f;
-#pragma unroll
-                    for (int h = 0; h < kHalves; ++h)
-                        if (!in)
-                            vreg[j][h] = VChunk{};
-                }
-            }
-            const v4i pw = {(int)K::pack(w[0], w[1]), (int)K::pack(w[2], w[3]), (int)K::pack(w[4], w[5]),
-                            (int)K::pack(w[6], w[7])};
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                for (int d = 0; d < kVWords; ++d) {
-                    uint32_t word[8];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        word[j] = ((const uint32_t*)&vreg[j][h])[d];
-                    if (!FP8) {  // two elements of eight keys
-                        v4i lo, hi;
+                        if (!(mask >> (8 * n + j) & 1)) {
+                            vsc[n][j] = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            lo[j] = (int)__builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x05040100u);
-                            hi[j] = (int)__builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x07060302u);
+                            for (int h = 0; h < kHalves; ++h)
+                                vreg[n][j][h] = VChunk{};
                         }
-                        o[kPer * h + 2 * d] = K::mfma(lo, pw, o[kPer * h + 2 * d]);
-                        o[kPer * h + 2 * d + 1] = K::mfma(hi, pw, o[kPer * h + 2 * d + 1]);
-                    } else {  // four elements of eight keys
-                        v4i e[4];
+            }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t lo = __builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x05010400u);
-                            const uint32_t hi = __builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x07030602u);
-                            e[0][j] = (int)fp8x2_to_bf16<false>(lo);
-                            e[1][j] = (int)fp8x2_to_bf16<true>(lo);
-                            e[2][j] = (int)fp8x2_to_bf16<false>(hi);
-                            e[3][j] = (int)fp8x2_to_bf16<true>(hi);
-                        }
+            for (int n = 0; n < NT; ++n) {
+                // the weights as a value of the type and the rest: the products'
+                // error is that of their sums (one rounding alone would add an
+                // error as large as the result's)
+                v4i ph, pl;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            o[kPer * h + 4 * d + i] = K::mfma(e[i], pw, o[kPer * h + 4 * d + i]);
+                for (int j = 0; j < 4; ++j) {
+                    float w0 = exp2_(x[n][2 * j] - ref), w1 = exp2_(x[n][2 * j + 1] - ref);
+                    l += w0 + w1;
+                    if (FP8) {
+                        w0 *= vsc[n][2 * j];
+                        w1 *= vsc[n][2 * j + 1];
                     }
+                    int hi, lo;
+                    K::split(w0, w1, hi, lo);
+                    ph[j] = hi;
+                    pl[j] = lo;
                 }
+                auto add = [&](int i, const v4i& e) {
+                    o[i] = K::mfma(e, ph, o[i]);
+                    o[i] = K::mfma(e, pl, o[i]);
+                };
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                    for (int d = 0; d < kVWords; ++d) {
+                        uint32_t word[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            word[j] = ((const uint32_t*)&vreg[n][j][h])[d];
+                        if (!FP8) {  // two elements of eight keys
+                            v4i lo, hi;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                lo[j] = (int)__builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x05040100u);
+                                hi[j] = (int)__builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x07060302u);
+                            }
+                            add(kPer * h + 2 * d, lo);
+                            add(kPer * h + 2 * d + 1, hi);
+                        } else {  // four elements of eight keys
+                            v4i e[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t lo = __builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x05010400u);
+                                const uint32_t hi = __builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x07030602u);
+                                e[0][j] = (int)fp8x2_to_bf16<false>(lo);
+                                e[1][j] = (int)fp8x2_to_bf16<true>(lo);
+                                e[2][j] = (int)fp8x2_to_bf16<false>(hi);
+                                e[3][j] = (int)fp8x2_to_bf16<true>(hi);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                add(kPer * h + 4 * d + i, e[i]);
+                        }
+                    }
+            }
             if (more) {
-                load_v(tile + kWaves, idv);
-                idv = idv_next;
+                load_v(key0 + kStep, ids);
+                ids = next;
             }
         }
 
@@ -531,24 +636,24 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_decode_kerne
         const float all_ref = all_m == -__builtin_inff() ? 0.0f : all_m;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            f[w] = exp2_(ml[w].x - all_ref);
+            f[w] = exp2_(ml[w].x - (all_ref + K::kShift));
             all_l += ml[w].y * f[w];
         }
-        const bool done = !p.cut || (unit0 == 0 && unit1 == units);
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (segment > 0);
+        const bool done = !CUT || (unit0 == 0 && unit1 == units);
+        const int64_t slot = 2 * (int64_t)me + (segment > 0);
         const float inv = all_l == 0.0f ? 0.0f : 1.0f / all_l;  // NaN stays
-        // this wave takes register `wave` of each product: elements kPer * (4 g + wave) .. of column c16
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
+        // register r of the products of a half: elements kPer * (4 g + r) .. of column c16
+        for (int it = wave; it < 4 * kHalves; it += kWaves) {
+            const int r = it & 3, h = it >> 2;
             float y[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 y[i] = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWaves; ++w)
-                    y[i] += sh_o[w][4 * (kPer * h + i) + wave][lane] * f[w];
+                    y[i] += sh_o[w][4 * (kPer * h + i) + r][lane] * f[w];
             }
-            const int d = 128 * h + kPer * (4 * g + wave);
+            const int d = 128 * h + kPer * (4 * g + r);
             if (c16 < heads && d < a.D) {
                 if (done) {
                     uint32_t* dst = (uint32_t*)((uint16_t*)a.out + b * a.o_bs + (head0 + c16) * a.o_hs + d);
@@ -573,70 +678,115 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 1 : 2) void attn_decode_kerne
     }
 }
 
-// One wave per (sequence, query head): nothing to do where the head's work lay
-// in one workgroup; zeros where there was none.
-template <bool F16>
-__global__ __launch_bounds__(256) void attn_join_kernel(const Plan p)
+// Joins what was cut: a workgroup takes ROWS query heads of one (sequence, kv
+// head, block of 16).  ROWS 16: a wave takes a head at a time; 1: the waves split its parts.  Nothing
+// to do where the work lay in one workgroup; zeros where there was none.
+template <bool F16, int ROWS>
+__global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(const Plan p, const int32_t parts)
 {
+    using K = Kind<F16 ? W4A8_TYPE_FP16 : W4A8_TYPE_BF16>;
+    constexpr int kSplit = ROWS == 1 ? kJoinWaves : 1;  // waves that share a row
+    constexpr int kMost = 4;                        // elements of a lane
+    __shared__ float sh[kSplit][64 * kMost];
     const AttnArgs& a = p.a;
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= (int64_t)a.B * a.q_heads)
-        return;
-    const int b = (int)(row / a.q_heads), head = (int)(row - (int64_t)b * a.q_heads);
-    const int kv = head / p.group, in_group = head - kv * p.group;
-    const int item = kv * p.blocks + in_group / kHeads, col = in_group % kHeads;
-    uint16_t* out = (uint16_t*)a.out + b * a.o_bs + head * a.o_hs;
-    const int64_t total = p.header[0], in_use = p.header[1];
-    const int64_t b0 = p.header[2 + b], units = (p.header[3 + b] - b0) / p.items;
-    if (units == 0) {
-        for (int d = lane; d < a.D; d += 64)
-            out[d] = 0;
-        if (lane == 0 && a.lse != nullptr)
-            a.lse[row] = -__builtin_inff();
-        return;
-    }
-    // workgroup w begins at floor(total * w / in_use)
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = (int64_t)blockIdx.x / parts;  // sequence and item
+    const int b = (int)(id / p.items), item = (int)(id - (int64_t)b * p.items);
+    const int kv = item / p.blocks, head0 = kv * p.group + (item - kv * p.blocks) * kHeads;
+    const int heads = min(kHeads, (kv + 1) * p.group - head0);
+    const int64_t total = p.header[0];
+    const int in_use = (int)p.header[1];
+    const int64_t b0 = p.header[2 + b], units = quotient(p.header[3 + b] - b0, p.items);
     const int64_t u0 = b0 + item * units, u1 = u0 + units;
-    const int64_t w0 = ((u0 + 1) * in_use + total - 1) / total - 1, w1 = (u1 * in_use + total - 1) / total - 1;
-    if (w0 == w1)
-        return;
-    auto slot_of = [&](int64_t w) {  // the work is the workgroup's first, or for w0 perhaps a later one
-        return 2 * w + (w == w0 && total * w / in_use < u0);
-    };
-    float m = -__builtin_inff();
-    for (int64_t w = w0 + lane; w <= w1; w += 64)
-        m = fmaxf(m, p.part_ml[slot_of(w) * kHeads + col].x);
-    m = group_max<64>(m);
-    const float ref = m == -__builtin_inff() ? 0.0f : m;
-    float l = 0.0f;
-    for (int64_t w = w0 + lane; w <= w1; w += 64) {
-        const float2 ml = p.part_ml[slot_of(w) * kHeads + col];
-        l += ml.y * exp2_(ml.x - ref);
+    int w0 = 0, w1 = -1, later = 0;  // workgroups that hold a part; w0's may not be its first
+    if (units > 0) {
+        w0 = holder_of(total, in_use, u0);
+        w1 = holder_of(total, in_use, u1 - 1);
+        later = begin_of(total, in_use, w0) < u0;
+        if (w0 == w1)
+            return;
     }
-    l = group_sum<64>(l);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int d = lane; d < a.D; d += 64) {
-        float y = 0.0f;
-        for (int64_t w = w0; w <= w1; ++w) {
-            const int64_t at = slot_of(w) * kHeads + col;
-            y += p.part_o[at * a.D + d] * exp2_(p.part_ml[at].x - ref);
+    auto slot_of = [&](int w) { return (2 * (int64_t)w + (w == w0 ? later : 0)) * kHeads; };
+    const int first = (int)((int64_t)blockIdx.x - id * parts) * ROWS + (ROWS == 1 ? 0 : wave);
+    for (int row = first; row < heads && row < first + ROWS; row += ROWS == 1 ? 1 : kJoinWaves) {
+        float m = -__builtin_inff(), l = 0.0f, y[kMost] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int w = w0 + lane; w <= w1; w += 64)
+            m = fmaxf(m, p.part_ml[slot_of(w) + row].x);
+        m = group_max<64>(m);
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+        for (int at = w0; at <= w1; at += 64) {
+            float f = 0.0f;
+            if (at + lane <= w1) {
+                const float2 ml = p.part_ml[slot_of(at + lane) + row];
+                f = exp2_(ml.x - ref);
+                l += ml.y * f;
+            }
+            const int n = min(64, w1 - at + 1);
+            for (int i0 = ROWS == 1 ? wave : 0; i0 < n; i0 += 4 * kSplit) {
+                float v[4][kMost];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float* src = p.part_o + (slot_of(at + min(i0 + j * kSplit, n - 1)) + row) * a.D;
+#pragma unroll
+                    for (int k = 0; k < kMost; ++k)
+                        v[j][k] = lane + 64 * k < a.D ? src[lane + 64 * k] : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = i0 + j * kSplit;
+                    if (i < n) {
+                        const float g = __shfl(f, i, 64);
+#pragma unroll
+                        for (int k = 0; k < kMost; ++k)
+                            y[k] = fmaf(v[j][k], g, y[k]);
+                    }
+                }
+            }
         }
-        y *= inv;
-        out[d] = F16 ? __builtin_bit_cast(uint16_t, (_Float16)y) : (uint16_t)f32x2_to_bf16x2(y, 0.0f);
+        l = group_sum<64>(l);
+        if (ROWS == 1) {
+#pragma unroll
+            for (int k = 0; k < kMost; ++k)
+                sh[wave][64 * k + lane] = y[k];
+            __syncthreads();
+            if (wave != 0)
+                return;
+#pragma unroll
+            for (int k = 0; k < kMost; ++k) {
+                y[k] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kSplit; ++w)
+                    y[k] += sh[w][64 * k + lane];
+            }
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* out = (uint16_t*)a.out + b * a.o_bs + (head0 + row) * a.o_hs;
+#pragma unroll
+        for (int k = 0; k < kMost; ++k)
+            if (lane + 64 * k < a.D)
+                out[lane + 64 * k] = (uint16_t)K::pack(y[k] * inv, 0.0f);
+        if (lane == 0 && a.lse != nullptr)
+            a.lse[(int64_t)b * a.q_heads + head0 + row] = (m + __builtin_amdgcn_logf(l)) * kLn2;
     }
-    if (lane == 0 && a.lse != nullptr)
-        a.lse[row] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 namespace {
 
-constexpr int64_t kWorkgroups = 512;  // two for each CU
-
-// Cut over workgroups unless no sequence can be longer than one unit.
-bool cuts(int64_t max_len)
+// workgroups that share what is cut: one or two for each CU, as their registers allow
+int64_t workgroups_of(int64_t D)
 {
-    return max_len > kUnit;
+    return D > 128 ? 256 : 512;
+}
+
+// Whether sequences are cut over workgroups, by what one of the n (sequence, kv
+// head) can hold at most.  Uncut, one CU streams 45 GB/s of it after 7 us; cut,
+// all share it, but the partial results and their join take 12 us and more.
+// Measured (bf16, D 128, 8 kv heads; uncut / cut, us): 1 sequence of 500
+// keys 9.7 / 12.5, of 1000 14.7 / 13.0; 8 of 1000 16.5 / 17.5, of 2000 26.8 /
+// 21.7; 32 of 2000 51.9 / 60.5, of 125 to 4000 65.9 / 46.3.
+bool cuts(int64_t n, int64_t bytes)
+{
+    return bytes > (n >= 256 ? 1 << 20 : n >= 64 ? 1 << 19 : 1 << 18);
 }
 
 Plan plan(void* ws, const AttnArgs& a, size_t* bytes)
@@ -646,9 +796,10 @@ Plan plan(void* ws, const AttnArgs& a, size_t* bytes)
     p.group = a.q_heads / a.kv_heads;
     p.blocks = (p.group + kHeads - 1) / kHeads;
     p.items = a.kv_heads * p.blocks;
-    int64_t longest = (int64_t)a.max_pages * a.page_size;
-    p.cut = cuts(longest);
-    p.workgroups = (int32_t)(p.cut ? kWorkgroups : (int64_t)a.B * p.items);
+    const int64_t longest = (int64_t)a.max_pages * a.page_size;
+    const int64_t row = 2 * a.D * (a.cache_type == W4A8_TYPE_E4M3 ? 1 : 2);
+    p.cut = cuts((int64_t)a.B * p.items, row * (a.window > 0 && a.window < longest ? a.window : longest));
+    p.workgroups = (int32_t)(p.cut ? workgroups_of(a.D) : (int64_t)a.B * p.items);
     // 2^l >= s > 2^(l - 1): m = ceil(2^(31 + l) / s) is below 2^32, and m s exceeds
     // 2^(31 + l) by less than s, so n m / 2^(31 + l) exceeds n / s by less than
     // n / 2^(31 + l) <= n 2^-31 / s, which is below 1 / s and carries over no integer
@@ -660,21 +811,29 @@ Plan plan(void* ws, const AttnArgs& a, size_t* bytes)
     api::Carve c(ws);
     if (p.cut) {
         p.header = c.take<int64_t>((size_t)a.B + 3);
-        p.part_o = c.take<float>((size_t)(2 * kWorkgroups) * kHeads * a.D);
-        p.part_ml = c.take<float2>((size_t)(2 * kWorkgroups) * kHeads);
+        p.part_o = c.take<float>((size_t)(2 * workgroups_of(a.D)) * kHeads * a.D);
+        p.part_ml = c.take<float2>((size_t)(2 * workgroups_of(a.D)) * kHeads);
     }
     *bytes = c.used;
     return p;
 }
 
+template <int CT, int DP, bool PAD, bool RUNS>
+void launch4(const Plan& p, hipStream_t s)
+{
+    const dim3 grid((unsigned)p.workgroups);
+    if (p.cut)
+        hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, RUNS, true>), grid, dim3(64 * waves_of(DP, true)), 0, s, p);
+    else
+        hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, RUNS, false>), grid, dim3(64 * waves_of(DP, false)), 0, s, p);
+}
 template <int CT, int DP, bool PAD>
 void launch3(const Plan& p, hipStream_t s)
 {
-    const dim3 grid((unsigned)p.workgroups);
     if (p.a.page_size % 8 == 0)
-        hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, true>), grid, dim3(kThreads), 0, s, p);
+        launch4<CT, DP, PAD, true>(p, s);
     else
-        hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, false>), grid, dim3(kThreads), 0, s, p);
+        launch4<CT, DP, PAD, false>(p, s);
 }
 template <int CT, int DP>
 void launch2(const Plan& p, hipStream_t s)
@@ -697,6 +856,19 @@ void launch1(const Plan& p, hipStream_t s)
         launch2<CT, 128>(p, s);
     else
         launch2<CT, 256>(p, s);
+}
+
+template <bool F16>
+hipError_t launch_join(const Plan& p, hipStream_t s)
+{
+    // few: a workgroup for each head, for whose parts many waves can ask at once
+    const int64_t n = (int64_t)p.a.B * p.items;
+    const int32_t rows = p.group < kHeads ? p.group : kHeads;
+    if (n >= 256)
+        hipLaunchKernelGGL((attn_join_kernel<F16, kHeads>), dim3((unsigned)n), dim3(64 * kJoinWaves), 0, s, p, 1);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<F16, 1>), dim3((unsigned)(n * rows)), dim3(64 * kJoinWaves), 0, s, p, rows);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -723,12 +895,7 @@ hipError_t launch_attn_decode(const AttnArgs& a, void* ws, hipStream_t s)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.cut)
         return e;
-    const dim3 grid((unsigned)(((int64_t)a.B * a.q_heads + 3) / 4));
-    if (a.q_type == W4A8_TYPE_FP16)
-        hipLaunchKernelGGL((attn_join_kernel<true>), grid, dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((attn_join_kernel<false>), grid, dim3(256), 0, s, p);
-    return hipGetLastError();
+    return a.q_type == W4A8_TYPE_FP16 ? launch_join<true>(p, s) : launch_join<false>(p, s);
 }
 
 }  // namespace w4a8
