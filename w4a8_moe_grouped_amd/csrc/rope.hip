@@ -5,9 +5,9 @@
 // one token and some of its rows (the heads of q, then k, then v).  Its lanes
 // first make the token's cosines and sines, one pair each, into the wave's own
 // part of LDS, so that their 40 operations are done once for all the wave's
-// rows; then 8 lanes (16 for D > 128) hold a row, two chunks of 8 elements
-// each, which for pairs of halves are the two partners, so that all accesses
-// are 16 bytes and no element crosses lanes.
+// rows; then 8 lanes (16 for D > 128) hold a row in chunks of 16 bytes,
+// neighbouring lanes' chunks side by side; for pairs of halves a lane holds both
+// partners, so that no element crosses lanes.
 //
 // The angle's turns are reduced in 64 bits (at position 10^6 an fp32 angle is
 // off by 0.03), sine and cosine of what is left, at most an eighth of a turn,
@@ -45,61 +45,43 @@ __device__ __forceinline__ float2 cos_sin(double turns, float m)
     return make_float2(m * (n == 1 || n == 2 ? -cq : cq), m * (n >= 2 ? -sq : sq));
 }
 
+// 16 bytes of a row
 template <int TYPE>
 struct Elem;
 template <>
 struct Elem<W4A8_TYPE_FP32> {
     typedef float T;
-    struct Raw {
-        v4i a, b;
-    };
-    static __device__ __forceinline__ Raw load(const T* p) { return Raw{ldg16(p), ldg16(p + 4)}; }
-    static __device__ __forceinline__ float get(const Raw& r, int i)
+    static __device__ __forceinline__ float get(const v4i& r, int i) { return __int_as_float(r[i]); }
+    static __device__ __forceinline__ v4i pack(const float* f)
     {
-        return __int_as_float(i < 4 ? r.a[i & 3] : r.b[i & 3]);
-    }
-    static __device__ __forceinline__ float one(const T* p) { return *p; }
-    static __device__ __forceinline__ void store(T* p, const float* f)
-    {
-        *(float4*)p = make_float4(f[0], f[1], f[2], f[3]);
-        *(float4*)(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+        return v4i{__float_as_int(f[0]), __float_as_int(f[1]), __float_as_int(f[2]), __float_as_int(f[3])};
     }
 };
 template <>
 struct Elem<W4A8_TYPE_BF16> {
-    typedef uint16_t T;
-    struct Raw {
-        v4i a;
-    };
-    static __device__ __forceinline__ Raw load(const T* p) { return Raw{ldg16(p)}; }
-    static __device__ __forceinline__ float get(const Raw& r, int i)
+    typedef __bf16 T;
+    static __device__ __forceinline__ float get(const v4i& r, int i)
     {
-        const uint32_t d = (uint32_t)r.a[i >> 1];
+        const uint32_t d = (uint32_t)r[i >> 1];
         return __uint_as_float(i & 1 ? d & 0xFFFF0000u : d << 16);
     }
-    static __device__ __forceinline__ float one(const T* p) { return bf16_to_f32(*p); }
-    static __device__ __forceinline__ void store(T* p, const float* f)
+    static __device__ __forceinline__ v4i pack(const float* f)
     {
-        *(v4i*)p = v4i{(int)f32x2_to_bf16x2(f[0], f[1]), (int)f32x2_to_bf16x2(f[2], f[3]),
-                       (int)f32x2_to_bf16x2(f[4], f[5]), (int)f32x2_to_bf16x2(f[6], f[7])};
+        return v4i{(int)f32x2_to_bf16x2(f[0], f[1]), (int)f32x2_to_bf16x2(f[2], f[3]), (int)f32x2_to_bf16x2(f[4], f[5]),
+                   (int)f32x2_to_bf16x2(f[6], f[7])};
     }
 };
 template <>
 struct Elem<W4A8_TYPE_FP16> {
     typedef _Float16 T;
-    struct Raw {
-        v8h a;
-    };
-    static __device__ __forceinline__ Raw load(const T* p) { return Raw{__builtin_bit_cast(v8h, ldg16(p))}; }
-    static __device__ __forceinline__ float get(const Raw& r, int i) { return (float)r.a[i]; }
-    static __device__ __forceinline__ float one(const T* p) { return (float)*p; }
-    static __device__ __forceinline__ void store(T* p, const float* f)
+    static __device__ __forceinline__ float get(const v4i& r, int i) { return (float)__builtin_bit_cast(v8h, r)[i]; }
+    static __device__ __forceinline__ v4i pack(const float* f)
     {
         v8h h;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             h[i] = (_Float16)f[i];
-        *(v8h*)p = h;
+        return __builtin_bit_cast(v4i, h);
     }
 };
 
@@ -112,6 +94,7 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
     using E = Elem<TYPE>;
     typedef typename E::T T;
     constexpr int kGroups = 64 / LANES;
+    constexpr int kChunk = 16 / sizeof(T), kChunks = 16 / kChunk;  // elements of 16 bytes, and their number in a lane
     __shared__ float2 table[kWaves][kMaxPairs];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t item = (int64_t)blockIdx.x * kWaves + wave;
@@ -123,14 +106,16 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
     const int rows = a.q_heads + 2 * a.kv_heads;
     const int half = a.R / 2;
 
-    // this lane's two chunks of a row; the second may lie past its end
-    int e0 = 16 * c, e1 = 16 * c + 8;
-    if (LAYOUT == kHalves) {
-        const int turned = a.R / 16;  // lanes that hold partners
-        e0 = c < turned ? 8 * c : a.R + 16 * (c - turned);
-        e1 = c < turned ? 8 * c + half : e0 + 8;
+    // this lane's chunks of a row, neighbouring lanes' side by side; the last may lie past its end
+    int e[kChunks];
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        e[j] = kChunk * (c + LANES * j);
+        if (LAYOUT == kHalves) {  // two by two: partners, then what is not turned
+            const int pair = c + LANES * (j / 2), turned = half / kChunk;
+            e[j] = pair < turned ? kChunk * pair + (j & 1) * half : a.R + kChunk * (2 * (pair - turned) + (j & 1));
+        }
     }
-    const bool has0 = e0 < a.D, has1 = e1 < a.D;
 
     auto source = [&](int row) {
         const bool is_q = row < a.q_heads, is_k = row < a.q_heads + a.kv_heads;
@@ -138,16 +123,16 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
         const int head = is_q ? row : is_k ? row - a.q_heads : row - a.q_heads - a.kv_heads;
         return (const T*)r.p + t * r.ts + head * r.hs;
     };
-    typename E::Raw raw[PASSES][2];
+    v4i raw[PASSES][kChunks];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
         const int row = row0 + p * kGroups;
         if (row < rows) {
             const T* src = source(row);
-            if (has0)
-                raw[p][0] = E::load(src + e0);
-            if (has1)
-                raw[p][1] = E::load(src + e1);
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j)
+                if (e[j] < a.D)
+                    raw[p][j] = ldg16(src + e[j]);
         }
     }
     int64_t slot = -1;
@@ -172,65 +157,72 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
         const bool live = row < rows && (is_q || kept);
         float f[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            f[i] = live && has0 ? E::get(raw[p][0], i) : 0.0f;
-            f[8 + i] = live && has1 ? E::get(raw[p][1], i) : 0.0f;
-        }
+        for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                f[kChunk * j + i] = live && e[j] < a.D ? E::get(raw[p][j], i) : 0.0f;
         if (live && (is_q || is_k) && half > 0) {
             if (LAYOUT == kHalves) {
-                if (e0 < half) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 w = cs[e0 + i];
-                        const float x = f[i], y = f[8 + i];
-                        f[i] = x * w.x - y * w.y;
-                        f[8 + i] = fmaf(x, w.y, y * w.x);
+                for (int j = 0; j < kChunks; j += 2) {
+                    if (e[j] < half) {
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) {
+                            const float2 w = cs[e[j] + i];
+                            const float x = f[kChunk * j + i], y = f[kChunk * (j + 1) + i];
+                            f[kChunk * j + i] = x * w.x - y * w.y;
+                            f[kChunk * (j + 1) + i] = fmaf(x, w.y, y * w.x);
+                        }
                     }
                 }
             } else if (LAYOUT == kPairs) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int pair = 8 * c + i;
-                    if (pair < half) {
-                        const float2 w = cs[pair];
-                        const float x = f[2 * i], y = f[2 * i + 1];
-                        f[2 * i] = x * w.x - y * w.y;
-                        f[2 * i + 1] = fmaf(x, w.y, y * w.x);
+                for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+                    for (int i = 0; i < kChunk; i += 2) {
+                        if (e[j] + i < a.R) {
+                            const float2 w = cs[(e[j] + i) / 2];
+                            const float x = f[kChunk * j + i], y = f[kChunk * j + i + 1];
+                            f[kChunk * j + i] = x * w.x - y * w.y;
+                            f[kChunk * j + i + 1] = fmaf(x, w.y, y * w.x);
+                        }
                     }
-                }
             } else {
                 // halves that are no whole chunks: the partner, element by element
                 const T* src = source(row);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int e = 16 * c + i;
-                    if (e < a.R) {
-                        const bool first = e < half;
-                        const float2 w = cs[first ? e : e - half];
-                        const float y = E::one(src + (first ? e + half : e - half));
-                        f[i] = first ? f[i] * w.x - y * w.y : fmaf(y, w.y, f[i] * w.x);
+                for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) {
+                        const int at = e[j] + i;
+                        if (at < a.R) {
+                            const bool first = at < half;
+                            const float2 w = cs[first ? at : at - half];
+                            const float x = f[kChunk * j + i], y = (float)src[first ? at + half : at - half];
+                            f[kChunk * j + i] = first ? x * w.x - y * w.y : fmaf(y, w.y, x * w.x);
+                        }
                     }
-                }
             }
         }
         if (is_q && live) {
             T* dst = (T*)a.q_out + t * a.qo_ts + row * a.qo_hs;
-            if (has0)
-                E::store(dst + e0, f);
-            if (has1)
-                E::store(dst + e1, f + 8);
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j)
+                if (e[j] < a.D)
+                    *(v4i*)(dst + e[j]) = E::pack(f + kChunk * j);
         }
         if (a.kv_heads == 0)
             continue;
         const CacheRows& out = is_k ? a.kc : a.vc;
         const int head = is_k ? row - a.q_heads : row - a.q_heads - a.kv_heads;
         const int64_t at = page * out.ps + place * out.ts + head * out.hs;
-        if (!QUANT) {
+        static_assert(!QUANT || kChunks == 2, "codes come from 2-byte types");
+        if constexpr (!QUANT) {
             if (!is_q && live) {
-                if (has0)
-                    E::store((T*)out.p + at + e0, f);
-                if (has1)
-                    E::store((T*)out.p + at + e1, f + 8);
+#pragma unroll
+                for (int j = 0; j < kChunks; ++j)
+                    if (e[j] < a.D)
+                        *(v4i*)((T*)out.p + at + e[j]) = E::pack(f + kChunk * j);
             }
         } else {
             // the row's maximum; a NaN stays one
@@ -251,10 +243,11 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     q[i] = cvt_e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
-                if (has0)
-                    *(uint2*)(dst + e0) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-                if (has1)
-                    *(uint2*)(dst + e1) = make_uint2(q[4] | q[5] << 16, q[6] | q[7] << 16);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (e[j] < a.D)
+                        *(uint2*)(dst + e[j]) =
+                            make_uint2(q[4 * j] | q[4 * j + 1] << 16, q[4 * j + 2] | q[4 * j + 3] << 16);
                 if (c == 0)
                     out.scales[(page * a.kv_heads + head) * a.page_size + place] =
                         bad > 0.0f ? __builtin_nanf("") : scale_of(amax_c);
