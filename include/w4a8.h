@@ -633,9 +633,11 @@ int w4a8_fused_moe_stage_events(void* const* events, int n);
  *   b_e4m3             [R, K] e4m3 codes, R = N (2N with SwiGLU: gate rows, then up rows)
  *   b_scales           [ceil(R/128), K/128] fp32, one for each 128 x 128 block
  *   bias, activation, residual, out, ld_*, workspace   as w4a8_gemm_epilogue
- * K % 128 == 0, and with SwiGLU N % 128 == 0 (gate and up rows have blocks of
- * their own); other limits, workspace query and errors as w4a8_gemm_epilogue;
- * K <= 2^22.  A product is off by what the fp8 matrix instruction cuts (2^-13
+ * K % 128 == 0, K <= 2^22, M and R below 2^31, with SwiGLU N % 128 == 0 (gate
+ * and up rows have blocks of their own), the block scales below 2^32 bytes and
+ * each launch below 2^32 threads, which holds while ceil(M/16) * ceil(R/32) <
+ * 2^23 - 8 (UNSUPPORTED otherwise); workspace query (0 bytes at present) and
+ * errors as w4a8_gemm_epilogue.  A product is off by what the fp8 matrix instruction cuts (2^-13
  * of the largest of eight neighbours in K); sums over groups, scales and the
  * epilogue are in fp32, with one rounding at the end.
  */
@@ -687,7 +689,8 @@ int w4a8_rope_frequencies(int64_t rotary_dim, double base, int scaling, double f
  *   positions     [T] int32
  *   frequencies   [R/2] fp64, or NULL with rotary_dim 0 (a copy)
  * T, heads >= 0; D a multiple of 8 up to 256, R even, 0 <= R <= D; strides
- * non-negative multiples of 8; T <= 2^25, heads <= 4096 (UNSUPPORTED beyond).
+ * non-negative multiples of 8, those of out not 0 along more than one row;
+ * T <= 2^25, heads <= 4096, and T * heads below 2^29 (UNSUPPORTED beyond).
  */
 int w4a8_rope(const void* x, int type, int64_t T, int64_t heads, int64_t head_dim,
               int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
@@ -736,8 +739,8 @@ typedef struct {
  * block of the quantisation rule above: scale = max(amax, 1e-10) / 448, code =
  * e4m3(clamp(x * 448 / max(amax, 1e-10))); a NaN shows in the scale.  All
  * else in the cache stays as it was.
- * D = cache->head_dim; strides are non-negative multiples of 8; sizes and
- * errors as w4a8_rope, and q_heads + 2 * kv_heads <= 4096.  slots is 8-byte aligned.
+ * D = cache->head_dim; strides are non-negative multiples of 8, and rows that
+ * are written lie apart (no stride of 0 along more than one); sizes and errors as w4a8_rope, and q_heads + 2 * kv_heads <= 4096.  slots is 8-byte aligned.
  */
 int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
                    const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
@@ -764,12 +767,14 @@ int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
  *   workspace     partial results of sequences that are cut into parts (query
  *                 with NULL: a function of B, q_heads, kv_heads, D, max_pages
  *                 and page_size)
- * Scores and sums are in fp32; the softmax weights are rounded to q_type
- * before they meet the values.  How a batch is cut follows all its lengths, so
- * the order of a row's sums depends on the batch.
+ * Scores and sums are in fp32; a softmax weight meets the values as two parts of
+ * q_type, whose sum is off by 2^-16 (bf16) or 2^-22 (fp16) of it.  Each result
+ * is rounded once.  How a batch is cut follows all its lengths, so the order
+ * of a row's sums depends on the batch.
  * D = cache->head_dim: a multiple of 8 up to 256; q_heads a multiple of
  * kv_heads (INVALID_ARG otherwise); strides non-negative multiples of 8, B <=
- * 65536, q_heads <= 4096, max_pages * page_size <= 2^30 (UNSUPPORTED otherwise).
+ * 65536, q_heads <= 4096, B * kv_heads * ceil(q_heads / kv_heads / 16) <= 2^22,
+ * max_pages * page_size <= 2^30 (UNSUPPORTED otherwise).
  */
 int w4a8_attn_decode(const void* q, int q_type, int64_t B, int64_t q_heads, int64_t q_seq_stride,
                      int64_t q_head_stride, const w4a8_kv_cache* cache, const int32_t* page_table,

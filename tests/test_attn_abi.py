@@ -38,10 +38,27 @@ def test_gemm_fp8_refusals(L):
         assert _gemm(L, **kw) == INVALID, kw
     for kw in (dict(K=130), dict(K=1 << 23), dict(M=1 << 31), dict(N=1 << 31), dict(act=5, N=64), dict(w=ODD), dict(a=ODD),
                dict(out=ODD), dict(ws=ODD), dict(res=ODD), dict(bias=ODD), dict(M=1 << 30, N=1 << 30),
-               dict(N=(1 << 31) - 128, K=1 << 22)):
+               dict(N=(1 << 31) - 128, K=1 << 22), dict(M=(1 << 31) - 1, K=128, N=1 << 20)):
         assert _gemm(L, **kw) == UNSUPPORTED, kw
     assert _gemm(L, M=1, ws=None) == OK  # a query
     assert w4.gemm_fp8_workspace_bytes(4096, 7168, 2048, "swiglu") >= 0
+
+
+def test_gemm_fp8_sizes_that_always_fit(L):
+    """The sizes that include/w4a8.h promises, at random over the whole range."""
+    import random
+    rng = random.Random(5)
+    up = lambda a, b: -(-a // b)  # noqa: E731
+    checked = 0
+    for _ in range(20000):
+        act = rng.choice([0, 5])
+        M, N, G = (int(2 ** rng.uniform(0, top)) for top in (30.9, 29.9 if act else 30.9, 15))
+        N = up(N, 128) * 128 if act else N
+        R = 2 * N if act else N
+        if up(M, 16) * up(R, 32) < 2 ** 23 - 8 and up(R, 128) * G * 4 < 2 ** 32:
+            checked += 1
+            assert _gemm(L, M=M, K=128 * G, N=N, act=act, ws=None) == OK, (M, N, G, act)
+    assert checked > 1000
 
 
 def test_rope_frequencies_refusals(L):
@@ -64,7 +81,7 @@ def test_rope_refusals(L):
     assert _rope(L) == OK and _rope(L, T=3, H=0) == OK
     for kw in (dict(T=-1), dict(H=-1), dict(D=0), dict(type=3), dict(type=-1), dict(R=-2), dict(R=66), dict(R=3),
                dict(T=1, x=None), dict(T=1, out=None), dict(T=1, pos=None), dict(T=1, freq=None),
-               dict(T=1, out=A, os=(512, 64)), dict(T=1, out=A, os=(256, 72))):
+               dict(T=1, out=A, os=(512, 64)), dict(T=1, out=A, os=(256, 72)), dict(T=2, os=(0, 64)), dict(T=1, os=(256, 0))):
         assert _rope(L, **kw) == INVALID, kw
     for kw in (dict(D=60, R=2), dict(D=264, R=2), dict(T=1, x=ODD), dict(T=1, out=ODD), dict(xs=(-8, 64)), dict(xs=(256, 4)),
                dict(os=(256, 63)), dict(os=(-256, 64)), dict(T=(1 << 25) + 1), dict(H=4097), dict(pos=ctypes.c_void_p(0x10002)),
@@ -103,8 +120,10 @@ def test_kv_append_refusals(L):
         assert _append(L, cache=_cache(**kw)) == want, kw
     for kw in (dict(T=-1), dict(Hq=-1), dict(type=0), dict(type=2), dict(type=3), dict(q=None), dict(qo=None), dict(T=1, k=None),
                dict(T=1, v=None), dict(T=1, slots=None), dict(T=1, q=None, qo=None), dict(T=1, pos=None), dict(T=1, freq=None),
-               dict(R=66), dict(R=1), dict(qo=A, qos=(512, 64))):
+               dict(R=66), dict(R=1), dict(qo=A, qos=(512, 64)), dict(T=2, qos=(0, 64)), dict(T=1, qos=(256, 0))):
         assert _append(L, **kw) == INVALID, kw
+    for name in ("k_page", "k_token", "k_head", "v_page", "v_token", "v_head"):  # rows that are written lie apart
+        assert _append(L, cache=_cache(**{name + "_stride": 0})) == INVALID, name
     for kw in (dict(T=1 << 26), dict(Hq=4093), dict(qs=(4, 64)), dict(ks=(-8, 64)), dict(qos=(256, 1)), dict(k=ODD), dict(v=ODD),
                dict(q=ODD), dict(qo=ODD), dict(slots=ctypes.c_void_p(0x10004))):
         assert _append(L, **kw) == UNSUPPORTED, kw
@@ -131,6 +150,11 @@ def test_attn_decode_refusals(L):
                dict(os=(512, -64)), dict(table=ctypes.c_void_p(0x10002)), dict(lens=ctypes.c_void_p(0x10001)),
                dict(lse=ctypes.c_void_p(0x10002)), dict(ws=ODD)):
         assert _attn(L, **kw) == UNSUPPORTED, kw
+    assert _attn(L, n=2, os=(0, 64)) == INVALID and _attn(L, n=1, os=(512, 0)) == INVALID
+    assert _attn(L, n=65536, cache=_cache(kv_heads=65), Hq=65, ws=None) == UNSUPPORTED  # workgroups of one launch
+    assert _attn(L, n=65536, cache=_cache(kv_heads=64), Hq=1024, ws=None) == OK
+    assert _attn(L, n=65536, cache=_cache(kv_heads=64), Hq=1088, ws=None) == UNSUPPORTED
+    assert _attn(L, cache=_cache(k_head_stride=0, v_token_stride=0)) == OK  # read only: any strides
     assert _attn(L, cache=_cache(type=3, k_scales=0x10000, v_scales=0x10000)) == OK  # bf16 queries of codes
     assert _attn(L, cache=_cache(type=3, k_scales=0x10000, v_scales=0x10000), type=2) == INVALID
 

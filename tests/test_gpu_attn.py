@@ -444,6 +444,16 @@ def test_attn_decode_short_sequences_in_wide_tables(dev, kind, D, page):
         check_attn(make_batch(dev, lens, 8, 2, D, kind, page, extra=3000), window=70)
 
 
+def test_attn_decode_many_sequences_most_of_them_empty(dev):
+    """More sequences than the lanes of a wave, at the borders of 64 too, and long runs without a token."""
+    lens = [0] * 6400
+    for at, n in ((0, 3), (63, 300), (64, 1), (127, 128), (128, 129), (3000, 2000), (3001, 5), (6335, 40), (6399, 1000)):
+        lens[at] = n
+    check_attn(make_batch(dev, lens, 2, 1, 64, BF16, 64, extra=100))
+    lens[6399] = lens[0] = 0
+    check_attn(make_batch(dev, lens, 2, 1, 64, BF16, 64, extra=100), window=100)
+
+
 def test_attn_decode_one_page_each(dev):
     """Tables that hold no more than one unit are not cut."""
     for page in (16, 64, 128, 9):

@@ -18,6 +18,7 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 25;
 constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxHeadDim = 256;
 constexpr int64_t kMaxSequences = 65536;
+constexpr int64_t kMaxItems = (int64_t)1 << 22;  // workgroups of 512 threads in one launch
 constexpr int64_t kMaxPositions = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 48;  // elements
 
@@ -30,6 +31,12 @@ inline bool misaligned(const void* p, uintptr_t bytes)
 inline bool bad_stride(int64_t s)
 {
     return s < 0 || s % 8 != 0 || s > kMaxStride;
+}
+
+// rows that are written lie apart
+inline bool rows_meet(int64_t n, int64_t stride)
+{
+    return n > 1 && stride == 0;
 }
 
 // -1: proceed
@@ -86,9 +93,8 @@ int w4a8_gemm_fp8(const uint8_t* a_e4m3, const float* a_scales, int64_t M, int64
     const int64_t R = mul_sat(N, glu ? 2 : 1);
     if (K % W4A8_GROUP != 0 || K > kMaxDenseK || M > INT32_MAX || R > INT32_MAX || (glu && N % W4A8_GROUP != 0))
         return W4A8_ERR_UNSUPPORTED;
-    // one buffer resource holds the block scales; the grid is one launch's
-    if (mul_sat(ceil_div(R, W4A8_GROUP), K / W4A8_GROUP * 4) > UINT32_MAX ||
-        mul_sat(ceil_div(M, 16), ceil_div(N, 16)) > INT32_MAX || !w4a8::gemm_fp8_fits(M, K, N, activation))
+    // one buffer resource holds the block scales
+    if (mul_sat(ceil_div(R, W4A8_GROUP), K / W4A8_GROUP * 4) > UINT32_MAX || !w4a8::gemm_fp8_fits(M, K, N, activation))
         return W4A8_ERR_UNSUPPORTED;
     const int ws_rc = check_workspace(workspace, workspace_bytes, w4a8::gemm_fp8_workspace(M, K, N, activation));
     if (ws_rc >= 0)
@@ -169,6 +175,8 @@ int w4a8_rope(const void* x, int type, int64_t T, int64_t heads, int64_t head_di
         return W4A8_ERR_INVALID_ARG;
     if (any && x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
         return W4A8_ERR_INVALID_ARG;
+    if (any && (rows_meet(T, out_token_stride) || rows_meet(heads, out_head_stride)))
+        return W4A8_ERR_INVALID_ARG;
     const int rc = check_rotation(any ? T : 0, head_dim, rotary_dim, positions, frequencies);
     if (rc >= 0)
         return rc;
@@ -217,6 +225,14 @@ int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
     if (T > 0 && (k == nullptr || v == nullptr || slots == nullptr || (q == nullptr && q_heads > 0)))
         return W4A8_ERR_INVALID_ARG;
     if (q != nullptr && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
+        return W4A8_ERR_INVALID_ARG;
+    if (rows_meet(T, q_out_token_stride) && q_heads > 0)
+        return W4A8_ERR_INVALID_ARG;
+    if (T > 0 && rows_meet(q_heads, q_out_head_stride))
+        return W4A8_ERR_INVALID_ARG;
+    if (rows_meet(cache->num_pages, cache->k_page_stride) || rows_meet(cache->page_size, cache->k_token_stride) ||
+        rows_meet(cache->kv_heads, cache->k_head_stride) || rows_meet(cache->num_pages, cache->v_page_stride) ||
+        rows_meet(cache->page_size, cache->v_token_stride) || rows_meet(cache->kv_heads, cache->v_head_stride))
         return W4A8_ERR_INVALID_ARG;
     rc = check_rotation(T, cache->head_dim, rotary_dim, positions, frequencies);
     if (rc >= 0)
@@ -267,7 +283,8 @@ int w4a8_attn_decode(const void* q, int q_type, int64_t B, int64_t q_heads, int6
         return W4A8_ERR_INVALID_ARG;
     const int64_t D = cache->head_dim;
     if (B > kMaxSequences || q_heads > kMaxHeads || D % 8 != 0 || D > kMaxHeadDim ||
-        mul_sat(max_pages, cache->page_size) > kMaxPositions)
+        mul_sat(max_pages, cache->page_size) > kMaxPositions ||
+        mul_sat(B, cache->kv_heads * ceil_div(q_heads / cache->kv_heads, 16)) > kMaxItems)
         return W4A8_ERR_UNSUPPORTED;
     const int ws_rc = check_workspace(
         workspace, workspace_bytes,
@@ -278,6 +295,8 @@ int w4a8_attn_decode(const void* q, int q_type, int64_t B, int64_t q_heads, int6
     if (rc >= 0)
         return rc;
     if (q_type != (cache->type == W4A8_TYPE_E4M3 ? W4A8_TYPE_BF16 : cache->type) || window < 0 || ld_table < max_pages)
+        return W4A8_ERR_INVALID_ARG;
+    if (rows_meet(B, out_seq_stride) || (B > 0 && rows_meet(q_heads, out_head_stride)))
         return W4A8_ERR_INVALID_ARG;
     if (B > 0 && (q == nullptr || out == nullptr || q == out || page_table == nullptr || seq_lens == nullptr))
         return W4A8_ERR_INVALID_ARG;

@@ -233,18 +233,18 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
     int b = 0;
     int64_t b_first = 0;       // first unit of sequence b
     const int lens0 = CUT && lane < a.B ? a.lens[lane] : 0;  // of the first 64
+    auto units_at = [&](int i) {  // of sequence i, i % 64 == lane if it is below 64
+        int s, e;
+        span_of(a, i < 64 ? lens0 : i < a.B ? a.lens[i] : 0, s, e);
+        return (int64_t)units_of(s, e);
+    };
     if (CUT) {
         // every wave for itself, 64 sequences at a time: no barrier, and one load for a batch of up to 64
-        auto units_at = [&](int len) {
-            int s, e;
-            span_of(a, len, s, e);
-            return (int64_t)units_of(s, e);
-        };
-        auto len_at = [&](int i) { return i < a.B ? a.lens[i] : 0; };
-        const int64_t first = units_at(lens0);
+        const int64_t first = units_at(lane);
         int64_t total = first;
+#pragma unroll 4
         for (int at = 64; at < a.B; at += 64)
-            total += units_at(len_at(at + lane));
+            total += units_at(at + lane);
         total = uniform(wave_scan(total, lane), 63) * p.items;
         const int in_use = (int)min((int64_t)p.workgroups, total);
         if (blockIdx.x == 0 && wave == 0) {  // for the join
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
             }
             int64_t before = 0;
             for (int at = 0; at < a.B; at += 64) {
-                const int64_t n = at ? units_at(len_at(at + lane)) : first, sum = wave_scan(n, lane);
+                const int64_t n = at ? units_at(at + lane) : first, sum = wave_scan(n, lane);
                 if (at + lane < a.B)
                     p.header[3 + at + lane] = (before + sum) * p.items;
                 if (at + lane == 0)
@@ -268,7 +268,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         u_end = begin_of(total, in_use, me + 1);
         int64_t before = 0;
         for (int at = 0; at < a.B; at += 64) {
-            const int64_t n = at ? units_at(len_at(at + lane)) : first, sum = wave_scan(n, lane);
+            const int64_t n = at ? units_at(at + lane) : first, sum = wave_scan(n, lane);
             const uint64_t behind = __ballot((before + sum) * p.items > u);
             if (behind != 0) {
                 const int l = __builtin_ctzll(behind);
@@ -290,7 +290,13 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
             units = units_of(start, end);
             if (u >= b_first + (int64_t)units * p.items) {
                 b_first += (int64_t)units * p.items;
-                ++b;
+                // the next sequence with something in it: there is one, as u < u_end
+                uint64_t some = 0;
+                for (int at = (b + 1) & ~63; some == 0; at += 64) {
+                    some = __ballot(at + lane > b && at + lane < a.B && units_at(at + lane) > 0);
+                    if (some != 0)
+                        b = at + __builtin_ctzll(some);
+                }
                 --segment;
                 continue;
             }
