@@ -13,7 +13,7 @@
 // comes from 8 loads of a key's 16 bytes each (16 lanes read a row of 256
 // contiguous bytes) and byte permutations: product i takes the elements d = 8c + i of
 // the chunks c that the lanes hold.  So the cache goes straight into
-// registers, whole rows at a time, and LDS only joins the 4 waves at the end.
+// registers, whole rows at a time, and LDS only joins the waves at the end.
 //
 // The maximum is taken lazily: sums are rescaled only when a score passes the
 // reference by 2^8, which a vote of the wave finds out.
@@ -22,7 +22,12 @@
 // and cut evenly over the workgroups, from the lengths on the device.  A sequence and kv
 // head that falls into several workgroups leaves partial results, at most two
 // per workgroup, which a second launch joins in order; one that falls into one is
-// finished there.
+// finished there.  Where sequences are short by the table or the window (`cuts`),
+// a workgroup takes one sequence and kv head whole, and there is no second launch.
+//
+// 64 x 4096 keys, 64 / 8 heads of 128, bf16: 193 us (5.6 TB/s; a reduction reads
+// 6.1) and 4.7 for the second launch, which finds nothing to join; 655 MB of e4m3 in 16
+// sequences: 135 + 6.5 (rows of 128 bytes, 1 KB apart); one sequence of 1000: 7.9 + 4.6.
 #include "api_util.hpp"
 #include "common.hpp"
 #include "internal.hpp"
@@ -167,12 +172,14 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16(uint32_t d)
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, HIGH));
 }
 
-// tiles of 32 keys that a wave takes at a time: 16 to 32 KB of cache
-constexpr int tiles_of(int ct, int dp, bool cut)
+// tiles of 32 keys that a wave takes at a time: 16 KB of cache where registers
+// hold it (e4m3, D 128: 148 us with one, 142 with two; D 64: 185 and 179)
+constexpr int tiles_of(int ct, int dp)
 {
-    return dp == 256 ? 1 : ct == W4A8_TYPE_E4M3 || dp == 64 || !cut ? 2 : 1;
+    return dp != 256 && (ct == W4A8_TYPE_E4M3 || dp == 64) ? 2 : 1;
 }
-// waves of a workgroup
+// waves of a workgroup (uncut, 37 sequences under a window of 1000: 4 waves 21 us,
+// 8 waves 14.6; with D 256 a wave's registers leave room for 4)
 constexpr int waves_of(int dp, bool cut)
 {
     return cut || dp == 256 ? 4 : 8;
@@ -208,7 +215,7 @@ template <int CT, int DP, bool PAD, bool RUNS, bool CUT>
 __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void attn_decode_kernel(const Plan p)
 {
     constexpr int kWaves = waves_of(DP, CUT);
-    constexpr int NT = tiles_of(CT, DP, CUT);  // tiles of 32 keys that a wave takes at a time
+    constexpr int NT = tiles_of(CT, DP);  // tiles of 32 keys that a wave takes at a time
     constexpr int kTile = 32 * NT;
     using K = Kind<CT>;
     constexpr bool FP8 = CT == W4A8_TYPE_E4M3;
@@ -788,8 +795,8 @@ int64_t workgroups_of(int64_t D)
 // head) can hold at most.  Uncut, one CU streams 45 GB/s of it after 7 us; cut,
 // all share it, but the partial results and their join take 12 us and more.
 // Measured (bf16, D 128, 8 kv heads; uncut / cut, us): 1 sequence of 500
-// keys 9.7 / 12.5, of 1000 14.7 / 13.0; 8 of 1000 16.5 / 17.5, of 2000 26.8 /
-// 21.7; 32 of 2000 51.9 / 60.5, of 125 to 4000 65.9 / 46.3.
+// keys 9.1 / 12.5, of 1000 14.5 / 12.3; 8 of 1000 15.7 / 17.5, of 2000 26.8 /
+// 21.8; 32 of 2000 50.8 / 60.5, of 125 to 4000 65.9 / 45.5.
 bool cuts(int64_t n, int64_t bytes)
 {
     return bytes > (n >= 256 ? 1 << 20 : n >= 64 ? 1 << 19 : 1 << 18);

@@ -12,6 +12,10 @@
 // The angle's turns are reduced in 64 bits (at position 10^6 an fp32 angle is
 // off by 0.03), sine and cosine of what is left, at most an eighth of a turn,
 // by their Taylor series in fp32.
+//
+// 16384 tokens x 40 heads of 128, fp32: 128 us (5.25 TB/s, a copy 5.1; with 32
+// contiguous bytes a lane 154); append of 16384 tokens, 64 + 2 x 8 heads, to
+// e4m3: 126 us (5.1 TB/s); 64 tokens: 4.0 and 4.5 us, two memory latencies.
 #include "common.hpp"
 #include "internal.hpp"
 #include "w4a8.h"
