@@ -680,7 +680,7 @@ int w4a8_rope_frequencies(int64_t rotary_dim, double base, int scaling, double f
  * positions[t] * frequencies[i]:
  *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos)
  *   interleaved 0: a, b = elements i and i + R/2;  else 2i and 2i + 1
- * The other D - R elements are copied.  The angle is taken in 64 bits, sine
+ * The other D - R elements are copied.  The angle is taken in 64 bits, its sine
  * and cosine are good to 2e-7 at any position, and every output is rounded
  * once from fp32.
  *   x, out        [T, heads, D] of `type` (fp32, bf16 or fp16), element (t, h, d) at
@@ -703,7 +703,7 @@ int w4a8_rope(const void* x, int type, int64_t T, int64_t heads, int64_t head_di
  * k_token_stride + head * k_head_stride + d (elements; the same for v), so
  * both [pages, tokens, heads, D] and [pages, heads, tokens, D] serve, and
  * views of one buffer.  With type W4A8_TYPE_E4M3 the elements are codes and
- * each token and head has one fp32 scale, k_scales and v_scales
+ * each token and head has one positive fp32 scale, k_scales and v_scales
  * [num_pages, kv_heads, page_size]; they are NULL for bf16 and fp16.  Codes
  * need no more than 8-byte alignment; strides are non-negative multiples of 8.
  * The struct itself is in host memory.
@@ -762,7 +762,8 @@ int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
  * nothing is left (a length of 0 or less), out is 0 and lse -inf.
  *   q, out        [B, q_heads, D] of q_type: bf16 or fp16, the cache's type, or
  *                 bf16 with an e4m3 cache; no overlap
- *   page_table    [B, max_pages] int32, row stride ld_table;  seq_lens [B] int32
+ *   page_table    [B, max_pages] int32, row stride ld_table;  seq_lens [B] int32;
+ *                 neither may change while the call runs
  *   lse           [B, q_heads] fp32, or NULL
  *   workspace     partial results of sequences that are cut into parts (query
  *                 with NULL: a function of B, q_heads, kv_heads, D, max_pages

@@ -343,6 +343,18 @@ def test_kv_append_codes_are_those_of_quantize_act(dev):
         assert torch.equal(scales.transpose(1, 2).reshape(-1, H)[:T], s[:, at])
 
 
+def test_cache_of_float8_tensors(dev):
+    """Codes may come as uint8 or as float8_e4m3fn."""
+    d = make_batch(dev, [40, 3], 4, 2, 64, "fp8", 16)
+    f8 = {k: v.view(FP8) if k in ("k_cache", "v_cache") else v for k, v in d.items()}
+    assert torch.equal(w4.attn_decode(**d)[0], w4.attn_decode(**f8)[0])
+    x = torch.randn(2, 2, 64, generator=gen(dev, 5), device=dev).to(BF16)
+    slots = torch.tensor([5, 17], device=dev)
+    before = d["k_cache"].clone()
+    w4.kv_append(x, x, f8["k_cache"], f8["v_cache"], slots, k_scales=d["k_scales"], v_scales=d["v_scales"])
+    assert not torch.equal(d["k_cache"], before)
+
+
 def test_kv_append_nan_shows_in_the_scale(dev):
     x = torch.randn(3, 2, 64, generator=gen(dev, 5), device=dev).to(BF16)
     x[1, 0, 9] = math.nan

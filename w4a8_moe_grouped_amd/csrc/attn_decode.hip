@@ -9,25 +9,26 @@
 // Which key is which row of S is free: rows 4g + r of its two products are
 // keys 8g + r and 8g + 4 + r, so the 8 scores a lane of quarter g ends up with
 // are those of keys 8g.. + 7, which are the K positions of the second product's
-// operand in that lane.  The operand's other side, element d of 8 keys in one lane,
-// comes from 8 loads of a key's 16 bytes each (16 lanes read a row of 256
-// contiguous bytes) and byte permutations: product i takes the elements d = 8c + i of
-// the chunks c that the lanes hold.  So the cache goes straight into
+// operand in that lane.  The operand's other side, element d of 8 keys in one
+// lane, comes from 8 loads of a key's 16 bytes each (16 lanes read a row of 256
+// contiguous bytes) and byte permutations: product i takes the elements d = 8c +
+// i of the chunks c that the lanes hold.  So the cache goes straight into
 // registers, whole rows at a time, and LDS only joins the waves at the end.
 //
 // The maximum is taken lazily: sums are rescaled only when a score passes the
 // reference by 2^8, which a vote of the wave finds out.
 //
-// Work: the batch's tiles are numbered (sequence, kv head, unit of 128 keys)
-// and cut evenly over the workgroups, from the lengths on the device.  A sequence and kv
-// head that falls into several workgroups leaves partial results, at most two
-// per workgroup, which a second launch joins in order; one that falls into one is
-// finished there.  Where sequences are short by the table or the window (`cuts`),
+// Work: the batch's tiles are numbered (sequence, kv head, unit of 128 keys) and
+// cut evenly over the workgroups, from the lengths on the device.  A sequence
+// and kv head that falls into several workgroups leaves partial results, at most
+// two per workgroup, which a second launch joins in order; one that falls into
+// one is finished there.  Where sequences are short by the table or the window (`cuts`),
 // a workgroup takes one sequence and kv head whole, and there is no second launch.
 //
 // 64 x 4096 keys, 64 / 8 heads of 128, bf16: 193 us (5.6 TB/s; a reduction reads
-// 6.1) and 4.7 for the second launch, which finds nothing to join; 655 MB of e4m3 in 16
-// sequences: 135 + 6.5 (rows of 128 bytes, 1 KB apart); one sequence of 1000: 7.9 + 4.6.
+// 6.1) and 4.7 for the second launch, which finds nothing to join; 655 MB of e4m3
+// in 16 sequences: 135 + 6.5 (rows of 128 bytes, 1 KB apart); one sequence of
+// 1000: 7.9 + 4.6.
 #include "api_util.hpp"
 #include "common.hpp"
 #include "internal.hpp"
@@ -43,7 +44,6 @@ constexpr int kHeads = 16;               // columns of a product
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
-typedef __bf16 v2b __attribute__((ext_vector_type(2)));
 
 struct Plan {
     AttnArgs a;
@@ -83,7 +83,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v, int l)
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-// floor(x / y), 0 <= x < 2^52, 0 < y < 2^31
+// floor(x / y) of values below 2^52 (a call has less than 2^46 units)
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)
 {
     int64_t q = (int64_t)((double)x / (double)y);
@@ -124,8 +124,8 @@ __device__ __forceinline__ float exp2_(float x)
 
 // The operand types of one kind of cache.  split: weights as a value cut to the
 // type and what the cut left, both above zero (zero times an infinite value
-// would be NaN).  fp16 holds the weights times 2^kShift: they stay below 2^(8 + kShift), and what is
-// added to a small one, below 2^-24, is 2^-31 of the reference.
+// would be NaN).  fp16 holds the weights times 2^kShift: they stay below 2^(8 +
+// kShift), and the least part, 2^-24, is 2^-31 of the reference.
 template <int CT>
 struct Kind;
 template <>
@@ -298,12 +298,15 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
             if (u >= b_first + (int64_t)units * p.items) {
                 b_first += (int64_t)units * p.items;
                 // the next sequence with something in it: there is one, as u < u_end
+                // (the bound ends the loop if the lengths change under it)
                 uint64_t some = 0;
-                for (int at = (b + 1) & ~63; some == 0; at += 64) {
+                for (int at = (b + 1) & ~63; some == 0 && at < a.B; at += 64) {
                     some = __ballot(at + lane > b && at + lane < a.B && units_at(at + lane) > 0);
                     if (some != 0)
                         b = at + __builtin_ctzll(some);
                 }
+                if (some == 0)
+                    break;
                 --segment;
                 continue;
             }
