@@ -101,12 +101,13 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
     constexpr int kChunk = 16 / sizeof(T), kChunks = 16 / kChunk;  // elements of 16 bytes, and their number in a lane
     __shared__ float2 table[kWaves][kMaxPairs];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t item = (int64_t)blockIdx.x * kWaves + wave;
-    const int64_t t = item / parts;
+    const uint32_t item = blockIdx.x * kWaves + wave;  // below 2^26
+    const int64_t t = item / (uint32_t)parts;
     if (t >= a.T)
         return;
     const int c = lane & (LANES - 1);
-    const int row0 = (int)(item - t * parts) * (kGroups * PASSES) + lane / LANES;
+    const int first = (int)(item - (uint32_t)t * parts) * (kGroups * PASSES);  // of the wave's rows
+    const int row0 = first + lane / LANES;
     const int rows = a.q_heads + 2 * a.kv_heads;
     const int half = a.R / 2;
 
@@ -151,11 +152,14 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
     __builtin_amdgcn_wave_barrier();  // one wave: LDS operations stay in order
     const float2* cs = table[wave];
     const bool kept = slot >= 0 && slot < a.num_slots;
-    const int64_t page = kept ? slot / a.page_size : 0;
+    const bool narrow = (uint64_t)(slot | a.page_size) <= UINT32_MAX;  // a division in 64 bits is a long one
+    const int64_t page = !kept ? 0 : narrow ? (uint32_t)slot / (uint32_t)a.page_size : slot / a.page_size;
     const int64_t place = kept ? slot - page * a.page_size : 0;
 
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
+        if (first + p * kGroups >= rows)
+            break;
         const int row = row0 + p * kGroups;
         const bool is_q = row < a.q_heads, is_k = !is_q && row < a.q_heads + a.kv_heads;
         const bool live = row < rows && (is_q || kept);
@@ -287,7 +291,7 @@ int lanes_of(const RopeArgs& a)
 int passes_of(const RopeArgs& a)
 {
     const int64_t rows = a.q_heads + 2 * (int64_t)a.kv_heads;
-    return a.T * ((rows * lanes_of(a) + 63) / 64) <= 4096 ? 1 : 4;
+    return a.T * ((rows * lanes_of(a) + 63) / 64) <= 8192 ? 1 : 4;
 }
 int64_t parts_of(const RopeArgs& a)
 {
