@@ -173,10 +173,11 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16(uint32_t d)
 }
 
 // tiles of 32 keys that a wave takes at a time: 16 KB of cache where registers
-// hold it (e4m3, D 128: 148 us with one, 142 with two; D 64: 185 and 179)
-constexpr int tiles_of(int ct, int dp)
+// hold it (e4m3, D 128: 148 us with one, 142 with two; D 64: 185 and 179; pages
+// without whole runs need registers for their places: 48 with one, 50 with two)
+constexpr int tiles_of(int ct, int dp, bool runs)
 {
-    return dp != 256 && (ct == W4A8_TYPE_E4M3 || dp == 64) ? 2 : 1;
+    return runs && dp != 256 && (ct == W4A8_TYPE_E4M3 || dp == 64) ? 2 : 1;
 }
 // waves of a workgroup (uncut, 37 sequences under a window of 1000: 4 waves 21 us,
 // 8 waves 14.6; with D 256 a wave's registers leave room for 4)
@@ -210,12 +211,15 @@ struct Chunk<16> {
 
 // CT: type of the cache.  DP: D rounded up to 64, 128 or 256.  PAD: D < DP (or
 // rows of codes that are not 16-byte aligned): chunks past D are not read.
-// RUNS: pages hold whole runs of 8 keys, so a lane's 8 keys share a page.
+// RUNS: pages hold whole runs of 8 keys, so a lane's 8 keys share a page.  Else
+// each lane looks up one key of the tile, ahead as for runs, and hands its page
+// round (64 x 4096 keys, bf16, pages of 60: 195 us; each lane looking up its own keys,
+// a load behind a load, 288).
 template <int CT, int DP, bool PAD, bool RUNS, bool CUT>
 __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void attn_decode_kernel(const Plan p)
 {
     constexpr int kWaves = waves_of(DP, CUT);
-    constexpr int NT = tiles_of(CT, DP);  // tiles of 32 keys that a wave takes at a time
+    constexpr int NT = tiles_of(CT, DP, RUNS);  // tiles of 32 keys that a wave takes at a time
     constexpr int kTile = 32 * NT;
     using K = Kind<CT>;
     constexpr bool FP8 = CT == W4A8_TYPE_E4M3;
@@ -390,15 +394,19 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         };
         // a lane's key row of tile t of a pair is key krun + 4 t + c16 % 4; its run of values is from key 8 g
         const int krun = 8 * (c16 >> 2), vrun = 8 * g;
+        // the pages of a tile: of the lane's runs, or without whole runs of the
+        // tile's key `lane`, which the lanes then ask each other for
         struct Ids {
             int k[NT], v[NT];
         };
         auto lookup_all = [&](int key0) {
             Ids id;
+            if (!RUNS)
+                id.k[0] = lane < kTile ? lookup(key0 + lane, 1) : -1;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                id.k[n] = RUNS ? lookup(key0 + 32 * n + krun, 8) : -1;
-                id.v[n] = RUNS ? lookup(key0 + 32 * n + vrun, 8) : -1;
+            for (int n = 0; RUNS && n < NT; ++n) {
+                id.k[n] = lookup(key0 + 32 * n + krun, 8);
+                id.v[n] = lookup(key0 + 32 * n + vrun, 8);
             }
             return id;
         };
@@ -414,8 +422,8 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                 } else {
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const int key = key0 + 32 * n + krun + 4 * t + (c16 & 3);
-                        const int one = lookup(key, 1);
+                        const int in = 32 * n + krun + 4 * t + (c16 & 3), key = key0 + in;
+                        const int one = __shfl(id.k[0], in, 64);
                         const int off = one >= 0 ? key - page_of(p, key) * a.page_size : 0;
                         load_k_row(n, t, kbase + max(one, 0) * kps + off * kts);
                     }
@@ -449,7 +457,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const int one = lookup(key + j, 1);
+                        const int one = __shfl(id.k[0], 32 * n + vrun + j, 64);
                         const int off = one >= 0 ? key + j - page_of(p, key + j) * a.page_size : 0;
                         load_v_row(n, j, vbase + max(one, 0) * vps + off * vts);
                         if (FP8) {
@@ -488,7 +496,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         if (key0 < seg1) {
             load_k(key0, ids);
             load_v(key0, ids);
-            if (RUNS && key0 + kStep < seg1)
+            if (key0 + kStep < seg1)
                 ids = lookup_all(key0 + kStep);
         }
         for (; key0 < seg1; key0 += kStep) {
@@ -518,7 +526,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                     }
             Ids next = ids;
             if (more) {
-                if (RUNS && key0 + 2 * kStep < seg1)
+                if (key0 + 2 * kStep < seg1)
                     next = lookup_all(key0 + 2 * kStep);
                 load_k(key0 + kStep, ids);
             }
