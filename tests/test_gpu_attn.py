@@ -110,6 +110,15 @@ def test_gemm_fp8_tiles(dev, M, K, N, act):
     check_gemm(ops, activation=act)
 
 
+# some row blocks times column counts around a multiple of 8 blocks of 32 and of 64
+@pytest.mark.parametrize("M, K, N", [(96, 1024, 5000), (70, 512, 545), (100, 384, 1030), (200, 1024, 1500),
+                                     (333, 256, 2050), (128, 2048, 991), (33, 256, 513), (65, 1024, 4100)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_gemm_fp8_several_row_blocks(dev, M, K, N, act):
+    N = N if act == "none" else N // 128 * 128
+    check_gemm(gemm_inputs(dev, M, K, 2 * N if act == "swiglu" else N), activation=act)
+
+
 @pytest.mark.parametrize("M", [1, 40, 300, 2500])
 def test_gemm_fp8_same_sign_and_extremes(dev, M):
     check_gemm(gemm_inputs(dev, M, 2048, 96 if M < 2000 else 2500, dist="positive"))
@@ -327,6 +336,22 @@ def test_kv_append_forms(dev, kind):
     check_append(dev, 2100, 20, 5, 200, 24, BF16, kind, 24, interleaved=True)
     if kind == "fp8":
         check_append(dev, 9, 4, 2, 128, 64, FP16, kind, 16)
+
+
+@pytest.mark.parametrize("T, heads, D, dtype", [(8193, 1, 128, FP32), (8200, 3, 256, BF16), (2731, 24, 64, FP16), (8192, 8, 128, BF16)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_many_tokens(dev, T, heads, D, dtype, interleaved):
+    """Either side of where a lane group takes four rows, and fewer rows than it could take."""
+    g = gen(dev, T)
+    x = torch.randn(T, heads, D, generator=g, device=dev).to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device=dev, dtype=torch.int32)
+    check_rope(x, pos, w4.rope_frequencies(D, device=dev), interleaved=interleaved)
+
+
+@pytest.mark.parametrize("kind", [BF16, "fp8"])
+@pytest.mark.parametrize("T, Hq, Hkv, D, page", [(8193, 2, 2, 256, 61), (8200, 1, 1, 128, 16), (4100, 4, 1, 256, 64)])
+def test_kv_append_many_tokens(dev, kind, T, Hq, Hkv, D, page):
+    check_append(dev, T, Hq, Hkv, D, 128, BF16, kind, page)
 
 
 def test_kv_append_codes_are_those_of_quantize_act(dev):

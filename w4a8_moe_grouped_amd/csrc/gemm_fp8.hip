@@ -11,7 +11,7 @@
 // rows), so the product of scales is a single multiplication for 16 rows.
 //
 // Few rows (fp8_rows_kernel): bound by the weight bytes and by latency.  1 x 7168 x
-// 10240: 13.8 us (5.3 TB/s); 64 x 8192 x 7168: 13.7 (4.5 TB/s); 333 x 1664 x 2050: 10.7.
+// 10240: 13.8 us (5.3 TB/s); 64 x 8192 x 7168: 13.7 (4.5 TB/s); 333 x 1664 x 2050: 7.6.
 // Many (fp8_tile_kernel): by the matrix unit, the promotion beside it and power.
 // 4096 x 7168 x 8192: 228 to 258 us by the box (1.9 to 2.1 PFLOP/s; the matrix
 // unit busy 53% of the cycles, other vector instructions 44%), with operands of zero 180;
@@ -74,8 +74,11 @@ __global__ __launch_bounds__(64 * WAVES) void fp8_rows_kernel(const DenseArgs a,
     const int mb = (int)blockIdx.x / col_blocks;
     const int64_t n0 = (int64_t)((int)blockIdx.x - mb * col_blocks) * (16 * kOut);
     const int64_t m0 = (int64_t)mb * (16 * MF);
+    if (n0 >= a.N)  // col_blocks may be rounded up
+        return;
 
-    // the first of this wave's items of the epilogue (slice, output fragment)
+    // the first of this wave's items of the epilogue (slice, output fragment);
+    // loads of all of them here cost more than they save (333 x 1664 x 2050: 9.8 -> 11.0 us)
     const int item_s = wave / kOut, item_f = wave - item_s * kOut;
     const int64_t item_m = m0 + 16 * item_s + c16, item_n = n0 + 16 * item_f + 4 * q;
     EpiOperands pre = {};
@@ -451,9 +454,9 @@ int64_t weight_rows(const DenseArgs& d)
 
 enum Kernel { kRows12, kRows14, kRows22, kRows24, kRows44, kRows44Two, kTiles128, kTiles128x256, kTiles256, kKernels };
 
-// Predicted times (us), fitted on MI355X over 584 sizes (M 1 to 4096, K 512 to
-// 8192, R 256 to 10240; the kernel they choose takes 4% more than the best on
-// average, 18% at the 95th percentile).  Few rows, blocks of 16 mf rows x 16 nf
+// Predicted times (us), fitted on MI355X (over 1071 sizes, M 1 to 4096, K 512 to
+// 8192, R 256 to 10240, the kernel they choose takes 3% more than the best on
+// average, 14% at the 95th percentile).  Few rows, blocks of 16 mf rows x 16 nf
 // weight rows: the latency of one block and the throughput of all, per_cu of
 // them a CU at a time, joined as the fourth root of the sum of fourth powers.  Tiles: rounds.
 struct Cost {
@@ -500,12 +503,22 @@ int choose(const DenseArgs& d)
     return best;
 }
 
+// Columns of blocks as fp8_rows_kernel numbers them.  Of several row blocks those
+// of one column share weight rows: with a multiple of 8 columns they run on one
+// XCD, whose L2 then serves all but the first (96 x 8192 x 5000: 21.7 -> 13.4 us,
+// 200 x 4096 x 1500: 12.4 -> 9.4, 333 x 1664 x 2050: 9.1 -> 7.6).
+int64_t numbered_columns(int64_t row_blocks, int64_t cols)
+{
+    return row_blocks > 1 && cols >= 16 ? (cols + 7) / 8 * 8 : cols;
+}
+
 template <int MF, int NF, int D, int WAVES, int AP>
 hipError_t launch_rows(const DenseArgs& a, hipStream_t s)
 {
     const bool glu = a.act == W4A8_ACT_SWIGLU;
-    const int64_t cols = 16 * (glu ? NF / 2 : NF), col_blocks = api::ceil_div(a.N, cols);
-    const dim3 grid((unsigned)(col_blocks * api::ceil_div(a.M, 16 * MF))), block(64 * WAVES);
+    const int64_t row_blocks = api::ceil_div(a.M, 16 * MF);
+    const int64_t col_blocks = numbered_columns(row_blocks, api::ceil_div(a.N, 16 * (glu ? NF / 2 : NF)));
+    const dim3 grid((unsigned)(col_blocks * row_blocks)), block(64 * WAVES);
     if (glu)
         hipLaunchKernelGGL((fp8_rows_kernel<MF, NF, true, D, WAVES, AP>), grid, block, 0, s, a, (int32_t)col_blocks);
     else
@@ -552,7 +565,8 @@ bool gemm_fp8_fits(int64_t M, int64_t K, int64_t N, int act)
     const int kernel = choose(d);
     const Cost& c = kCost[kernel];
     // workgroups have 512 threads at most
-    const int64_t blocks = api::ceil_div(M, 16 * c.mf) * api::ceil_div(weight_rows(d), 16 * c.nf);
+    const int64_t row_blocks = api::ceil_div(M, 16 * c.mf);
+    const int64_t blocks = row_blocks * numbered_columns(row_blocks, api::ceil_div(weight_rows(d), 16 * c.nf));
     return blocks < ((int64_t)1 << 23) - 8;
 }
 
