@@ -456,6 +456,37 @@ def test_attn_decode_heads(dev, kind, Hq, Hkv):
     check_attn(make_batch(dev, [300, 5, 0, 1000], Hq, Hkv, 128, kind, 16))
 
 
+# heads of 64 side by side are taken two by two where there are enough of them
+@pytest.mark.parametrize("kind", [BF16, FP16, "fp8"])
+@pytest.mark.parametrize("page, layout", [(16, "tokens"), (64, "heads"), (24, "joined"), (5, "tokens")])
+@pytest.mark.parametrize("group, Hkv", [(1, 8), (3, 4), (4, 8), (7, 6), (8, 4), (9, 4), (4, 5)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_attn_decode_heads_of_64(dev, kind, page, layout, group, Hkv, wide):
+    lens = LENS * (2 if wide else -(-512 // (Hkv * len(LENS))))
+    d = make_batch(dev, lens, group * Hkv, Hkv, 64, kind, page, layout, extra=5000 // page if wide else 2)
+    check_attn(d)
+    check_attn(d, window=70)
+
+
+@pytest.mark.parametrize("kind", [BF16, "fp8"])
+@pytest.mark.parametrize("lens", [[700] * 70, [3000] * 5 + [9, 0, 4100]])
+def test_attn_decode_heads_of_64_stay_apart(dev, kind, lens):
+    """A NaN in one head's keys or values shows in its own query heads and nowhere else."""
+    d = make_batch(dev, lens, 32, 8, 64, kind, 16)
+    whole = w4.attn_decode(**d, return_lse=True)
+    page = d["page_table"][0, 1].long()
+    for name, kv in (("k_cache", 2), ("v_cache", 5)):
+        at = d[name][page, 3, kv]
+        at[7] = 0x7F if kind == "fp8" else float("nan")
+    out, lse = w4.attn_decode(**d, return_lse=True)
+    bad = torch.zeros(len(lens), 32, dtype=torch.bool, device=dev)
+    bad[0, 8:12] = True
+    assert torch.equal(torch.isnan(lse), bad)
+    assert torch.isnan(out[0, 8:12]).all() and torch.isnan(out[0, 20:24, 7]).all()
+    bad[0, 20:24] = True
+    assert torch.equal(out[~bad], whole[0][~bad]) and torch.equal(lse[~bad], whole[1][~bad])
+
+
 @pytest.mark.parametrize("kind", [BF16, FP16, "fp8"])
 @pytest.mark.parametrize("window", [1, 5, 32, 100, 128, 129, 250, 100000])
 def test_attn_decode_window(dev, kind, window):

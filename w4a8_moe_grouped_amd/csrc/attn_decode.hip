@@ -51,6 +51,7 @@ struct Plan {
     int32_t items;          // kv heads x blocks
     int32_t workgroups;
     int32_t cut;            // whether sequences are cut over workgroups
+    int32_t pair;           // whether two kv heads of 64 are taken together: group and items count pairs
     uint32_t page_mul;      // floor(n / page_size) = (2 n page_mul) >> (32 + page_shift), n < 2^30
     int32_t page_shift;
     int64_t* header;        // total units, workgroups in use; then the first unit of each sequence
@@ -226,7 +227,10 @@ struct Chunk<16> {
 // each lane looks up one key of the tile, ahead as for runs, and hands its page
 // round (64 x 4096 keys, bf16, pages of 60: 195 us; each lane looking up its own keys,
 // a load behind a load, 288).
-template <int CT, int DP, bool PAD, bool RUNS, bool CUT>
+// PAIR: two neighbouring kv heads of 64 whose rows lie side by side are read as
+// rows of 128.  Each has its own scores, of which a lane keeps those of its
+// column's head; the sums are of both, and its head's are stored.
+template <int CT, int DP, bool PAD, bool RUNS, bool CUT, bool PAIR>
 __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void attn_decode_kernel(const Plan p)
 {
     constexpr int kWaves = waves_of(DP, CUT);
@@ -235,7 +239,9 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
     using K = Kind<CT>;
     constexpr bool FP8 = CT == W4A8_TYPE_E4M3;
     constexpr int kElem = FP8 ? 1 : 2;
+    static_assert(!PAIR || (DP == 128 && !PAD), "pairs of heads of 64");
     constexpr int kSteps = DP / 32;                       // MFMA steps over d
+    constexpr int kQSteps = PAIR ? kSteps / 2 : kSteps;   // of one head
     constexpr int kKLoads = FP8 ? DP / 64 : DP / 32;      // 16-byte loads of a lane's key row
     constexpr int kPer = DP == 64 ? 4 : 8;                // elements of a lane's chunk of a value row
     constexpr int kHalves = DP == 256 ? 2 : 1;            // chunks of a lane
@@ -286,7 +292,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         }
         if (me >= in_use)
             return;
-        if (FP8 || DP == 64)
+        if (FP8 || DP == 64 || PAIR)
             me = eighths(me, in_use);
         u = begin_of(total, in_use, me);
         u_end = begin_of(total, in_use, me + 1);
@@ -347,11 +353,11 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         const int32_t* table = a.table + b * a.ld_table;
 
         // the queries: column c16, positions of d as the keys' loads give them
-        v4i q[kSteps];
+        v4i q[kQSteps];
         {
             const uint16_t* src = (const uint16_t*)a.q + b * a.q_bs + (head0 + min(c16, heads - 1)) * a.q_hs;
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
+            for (int s = 0; s < kQSteps; ++s) {
                 const int d = FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
                 const bool in = c16 < heads && (!PAD || d < a.D);
                 q[s] = in ? ldg16(src + d) : v4i{0, 0, 0, 0};
@@ -363,8 +369,9 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
             o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         float m = -__builtin_inff(), ref = -K::kShift, l = 0.0f;
 
-        const char* const kbase = (const char*)a.kc.p + kv * a.kc.hs * kElem;
-        const char* const vbase = (const char*)a.vc.p + kv * a.vc.hs * kElem;
+        const int first_kv = PAIR ? 2 * kv : kv, second = PAIR && c16 >= p.group / 2;  // which of a pair is this column's
+        const char* const kbase = (const char*)a.kc.p + first_kv * a.kc.hs * kElem;
+        const char* const vbase = (const char*)a.vc.p + first_kv * a.vc.hs * kElem;
         const int64_t kts = a.kc.ts * kElem, kps = a.kc.ps * kElem, vts = a.vc.ts * kElem, vps = a.vc.ps * kElem;
 
         v4i kreg[NT][2][kKLoads];
@@ -460,7 +467,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                     if (id.v[n] >= 0)
                         mask |= ((0xFFu << lo) & (0xFFu >> (8 - hi)) & 0xFFu) << (8 * n);
                     if (FP8) {
-                        const int64_t at = ((int64_t)page * a.kv_heads + kv) * a.page_size + off;
+                        const int64_t at = ((int64_t)page * a.kv_heads + first_kv + second) * a.page_size + off;
 #pragma unroll
                         for (int j = 0; j < 8; j += 4) {
                             const float4 x = *(const float4*)(a.kc.scales + at + j), y = *(const float4*)(a.vc.scales + at + j);
@@ -475,7 +482,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                         const int off = one >= 0 ? key + j - page_of(p, key + j) * a.page_size : 0;
                         load_v_row(n, j, vbase + max(one, 0) * vps + off * vts);
                         if (FP8) {
-                            const int64_t at = ((int64_t)max(one, 0) * a.kv_heads + kv) * a.page_size + off;
+                            const int64_t at = ((int64_t)max(one, 0) * a.kv_heads + first_kv + second) * a.page_size + off;
                             ksc[n][j] = a.kc.scales[at];
                             vsc[n][j] = a.vc.scales[at];
                         }
@@ -515,12 +522,15 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         }
         for (; key0 < seg1; key0 += kStep) {
             const bool more = key0 + kStep < seg1;
-            v4f s[NT][2];
+            v4f s[NT][2], s1[PAIR ? NT : 1][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t) {
                     s[n][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (PAIR)
+                        s1[PAIR ? n : 0][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                }
 #pragma unroll
             for (int k = 0; k < kSteps; ++k)
 #pragma unroll
@@ -536,7 +546,8 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                         } else {
                             x = kreg[n][t][FP8 ? 0 : k];
                         }
-                        s[n][t] = K::mfma(x, q[k], s[n][t]);
+                        v4f& sum = k < kQSteps ? s[n][t] : s1[PAIR ? n : 0][t];
+                        sum = K::mfma(x, q[k % kQSteps], sum);
                     }
             Ids next = ids;
             if (more) {
@@ -550,7 +561,8 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    x[n][j] = s[n][j >> 2][j & 3] * (FP8 ? c * ksc[n][j] : c);
+                    x[n][j] = (PAIR && second ? s1[PAIR ? n : 0][j >> 2][j & 3] : s[n][j >> 2][j & 3]) *
+                              (FP8 ? c * ksc[n][j] : c);
             const bool whole = __all(mask == kAll);
             if (!whole) {
 #pragma unroll
@@ -691,8 +703,8 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                 for (int w = 0; w < kWaves; ++w)
                     y[i] += sh_o[w][4 * (kPer * h + i) + r][lane] * f[w];
             }
-            const int d = 128 * h + kPer * (4 * g + r);
-            if (c16 < heads && d < a.D) {
+            const int row_d = 128 * h + kPer * (4 * g + r), d = PAIR ? row_d & 63 : row_d;
+            if (c16 < heads && (PAIR ? row_d >> 6 == second : d < a.D)) {
                 if (done) {
                     uint32_t* dst = (uint32_t*)((uint16_t*)a.out + b * a.o_bs + (head0 + c16) * a.o_hs + d);
 #pragma unroll
@@ -827,6 +839,22 @@ bool cuts(int64_t n, int64_t bytes)
     return bytes > (n >= 256 ? 1 << 20 : n >= 64 ? 1 << 19 : 1 << 18);
 }
 
+// Whether kv heads of 64 are taken two by two, which reads rows of twice the bytes
+// and shares the softmax's instructions: where there are enough for all CUs, or
+// where they are cut and enough that the join does not get longer.  `placed`: by where the cache
+// lies too.  8 kv heads, single / paired, us: 64 x 4096 keys, e4m3 82 / 62, bf16 114 /
+// 112, up to 4096 55 / 42; 64 x 16384 308 / 226 and 434 / 397; 4 x 20000 37 / 29
+// and 41.6 / 39.1; but 32 x 4096 uncut 37 / 48 and 60 / 70; 2 x 20000 bf16 26 / 29.
+bool pairs(const AttnArgs& a, int32_t group, bool cut, bool placed)
+{
+    const int64_t n = (int64_t)a.B * a.kv_heads;
+    if (a.D != 64 || a.kv_heads % 2 != 0 || group > kHeads / 2 || n < (cut ? 32 : 512))
+        return false;
+    const uint64_t strides = a.kc.ps | a.kc.ts | a.vc.ps | a.vc.ts;
+    return !placed || (a.kc.hs == 64 && a.vc.hs == 64 && (strides & 15) == 0 &&
+                       (((uintptr_t)a.kc.p | (uintptr_t)a.vc.p) & 15) == 0);
+}
+
 Plan plan(void* ws, const AttnArgs& a, size_t* bytes)
 {
     Plan p = {};
@@ -835,8 +863,15 @@ Plan plan(void* ws, const AttnArgs& a, size_t* bytes)
     p.blocks = (p.group + kHeads - 1) / kHeads;
     p.items = a.kv_heads * p.blocks;
     const int64_t longest = (int64_t)a.max_pages * a.page_size;
-    const int64_t row = 2 * a.D * (a.cache_type == W4A8_TYPE_E4M3 ? 1 : 2);
-    p.cut = cuts((int64_t)a.B * p.items, row * (a.window > 0 && a.window < longest ? a.window : longest));
+    const int64_t row = 2 * a.D * (a.cache_type == W4A8_TYPE_E4M3 ? 1 : 2), n = (int64_t)a.B * p.items;
+    const int64_t most = row * (a.window > 0 && a.window < longest ? a.window : longest);
+    p.cut = cuts(n, most);
+    const bool paired_cut = p.cut || (pairs(a, p.group, false, false) && cuts(n / 2, 2 * most));
+    if (pairs(a, p.group, p.cut, true)) {
+        p.pair = 1;
+        p.cut = paired_cut;
+        p.group *= 2, p.items /= 2;
+    }
     p.workgroups = (int32_t)(p.cut ? workgroups_of(a.D) : (int64_t)a.B * p.items);
     // 2^l >= s > 2^(l - 1): m = ceil(2^(31 + l) / s) is below 2^32, and m s exceeds
     // 2^(31 + l) by less than s, so n m / 2^(31 + l) exceeds n / s by less than
@@ -847,7 +882,7 @@ Plan plan(void* ws, const AttnArgs& a, size_t* bytes)
     p.page_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + a.page_size - 1) / a.page_size);
     p.page_shift = l;
     api::Carve c(ws);
-    if (p.cut) {
+    if (paired_cut) {  // what a cache of any layout needs
         p.header = c.take<int64_t>((size_t)a.B + 3);
         p.part_o = c.take<float>((size_t)(2 * workgroups_of(a.D)) * kHeads * a.D);
         p.part_ml = c.take<float2>((size_t)(2 * workgroups_of(a.D)) * kHeads);
@@ -856,22 +891,22 @@ Plan plan(void* ws, const AttnArgs& a, size_t* bytes)
     return p;
 }
 
-template <int CT, int DP, bool PAD, bool RUNS>
+template <int CT, int DP, bool PAD, bool RUNS, bool PAIR>
 void launch4(const Plan& p, hipStream_t s)
 {
     const dim3 grid((unsigned)p.workgroups);
     if (p.cut)
-        hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, RUNS, true>), grid, dim3(64 * waves_of(DP, true)), 0, s, p);
+        hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, RUNS, true, PAIR>), grid, dim3(64 * waves_of(DP, true)), 0, s, p);
     else
-        hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, RUNS, false>), grid, dim3(64 * waves_of(DP, false)), 0, s, p);
+        hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, RUNS, false, PAIR>), grid, dim3(64 * waves_of(DP, false)), 0, s, p);
 }
-template <int CT, int DP, bool PAD>
+template <int CT, int DP, bool PAD, bool PAIR = false>
 void launch3(const Plan& p, hipStream_t s)
 {
     if (p.a.page_size % 8 == 0)
-        launch4<CT, DP, PAD, true>(p, s);
+        launch4<CT, DP, PAD, true, PAIR>(p, s);
     else
-        launch4<CT, DP, PAD, false>(p, s);
+        launch4<CT, DP, PAD, false, PAIR>(p, s);
 }
 template <int CT, int DP>
 void launch2(const Plan& p, hipStream_t s)
@@ -888,7 +923,9 @@ void launch2(const Plan& p, hipStream_t s)
 template <int CT>
 void launch1(const Plan& p, hipStream_t s)
 {
-    if (p.a.D <= 64)
+    if (p.pair)
+        launch3<CT, 128, false, true>(p, s);
+    else if (p.a.D <= 64)
         launch2<CT, 64>(p, s);
     else if (p.a.D <= 128)
         launch2<CT, 128>(p, s);
