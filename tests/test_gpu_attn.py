@@ -468,6 +468,20 @@ def test_attn_decode_heads_of_64(dev, kind, page, layout, group, Hkv, wide):
     check_attn(d, window=70)
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("page, start, gap", [(16, 8, 0), (5, 8, 0), (16, 0, 8), (16, 16, 16)])
+def test_attn_decode_codes_of_8_aligned_bytes(dev, D, page, start, gap):
+    """Codes that begin at, or whose tokens lie apart by, an odd multiple of 8 bytes."""
+    d = make_batch(dev, LENS * 3, 8, 2, D, "fp8", page, extra=3000 // page)
+    for name in ("k_cache", "v_cache"):
+        pages = d[name].shape[0]
+        buf = torch.zeros(start + pages * page * (2 * D + gap), dtype=d[name].dtype, device=dev)
+        view = buf[start:].view(pages, page, 2 * D + gap)[:, :, :2 * D].unflatten(2, (2, D))
+        view.copy_(d[name])
+        d[name] = view
+    check_attn(d)
+
+
 @pytest.mark.parametrize("kind", [BF16, "fp8"])
 @pytest.mark.parametrize("lens", [[700] * 70, [3000] * 5 + [9, 0, 4100]])
 def test_attn_decode_heads_of_64_stay_apart(dev, kind, lens):

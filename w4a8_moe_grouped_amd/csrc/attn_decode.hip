@@ -41,6 +41,7 @@ namespace {
 constexpr int kJoinWaves = 4;
 constexpr int kUnit = 128;               // keys: what work is counted and cut in
 constexpr int kHeads = 16;               // columns of a product
+enum Pad { kWhole, kShort, kApart };     // rows of the cache
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
@@ -221,8 +222,9 @@ struct Chunk<16> {
 
 }  // namespace
 
-// CT: type of the cache.  DP: D rounded up to 64, 128 or 256.  PAD: D < DP (or
-// rows of codes that are not 16-byte aligned): chunks past D are not read.
+// CT: type of the cache.  DP: D rounded up to 64, 128 or 256.  PAD: kShort if D <
+// DP, whose chunks past D are not read; kApart where rows of codes are not whole
+// pieces of 16 aligned bytes and go 8 by 8 (64 x 4096 keys, 8 heads of 96: 119 us, kShort 107).
 // RUNS: pages hold whole runs of 8 keys, so a lane's 8 keys share a page.  Else
 // each lane looks up one key of the tile, ahead as for runs, and hands its page
 // round (64 x 4096 keys, bf16, pages of 60: 195 us; each lane looking up its own keys,
@@ -230,7 +232,7 @@ struct Chunk<16> {
 // PAIR: two neighbouring kv heads of 64 whose rows lie side by side are read as
 // rows of 128.  Each has its own scores, of which a lane keeps those of its
 // column's head; the sums are of both, and its head's are stored.
-template <int CT, int DP, bool PAD, bool RUNS, bool CUT, bool PAIR>
+template <int CT, int DP, int PAD, bool RUNS, bool CUT, bool PAIR>
 __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void attn_decode_kernel(const Plan p)
 {
     constexpr int kWaves = waves_of(DP, CUT);
@@ -393,8 +395,9 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                 if (!FP8) {
                     const int d = 32 * i + 8 * g;
                     kreg[n][t][i] = !PAD || d < a.D ? load<v4i>(row + 2 * d) : v4i{0, 0, 0, 0};
-                } else if (!PAD) {
-                    kreg[n][t][i] = load<v4i>(row + 64 * i + 16 * g);
+                } else if (PAD != kApart) {
+                    const int d = 64 * i + 16 * g;
+                    kreg[n][t][i] = !PAD || d < a.D ? load<v4i>(row + d) : v4i{0, 0, 0, 0};
                 } else {
                     const int d = 64 * i + 16 * g;
                     const uint2 x = d < a.D ? *(const uint2*)(row + d) : make_uint2(0, 0);
@@ -891,7 +894,7 @@ Plan plan(void* ws, const AttnArgs& a, size_t* bytes)
     return p;
 }
 
-template <int CT, int DP, bool PAD, bool RUNS, bool PAIR>
+template <int CT, int DP, int PAD, bool RUNS, bool PAIR>
 void launch4(const Plan& p, hipStream_t s)
 {
     const dim3 grid((unsigned)p.workgroups);
@@ -900,7 +903,7 @@ void launch4(const Plan& p, hipStream_t s)
     else
         hipLaunchKernelGGL((attn_decode_kernel<CT, DP, PAD, RUNS, false, PAIR>), grid, dim3(64 * waves_of(DP, false)), 0, s, p);
 }
-template <int CT, int DP, bool PAD, bool PAIR = false>
+template <int CT, int DP, int PAD, bool PAIR = false>
 void launch3(const Plan& p, hipStream_t s)
 {
     if (p.a.page_size % 8 == 0)
@@ -912,19 +915,20 @@ template <int CT, int DP>
 void launch2(const Plan& p, hipStream_t s)
 {
     const AttnArgs& a = p.a;
-    const bool apart = CT == W4A8_TYPE_E4M3 &&  // code rows that are not 16-byte aligned
-                       (((uintptr_t)a.kc.p | (uintptr_t)a.vc.p | (uintptr_t)(a.kc.ps | a.kc.ts | a.kc.hs) |
-                         (uintptr_t)(a.vc.ps | a.vc.ts | a.vc.hs)) & 15) != 0;
-    if (a.D != DP || apart)
-        launch3<CT, DP, true>(p, s);
+    const bool apart = ((((uintptr_t)a.kc.p | (uintptr_t)a.vc.p | (uintptr_t)(a.kc.ps | a.kc.ts | a.kc.hs) |
+                          (uintptr_t)(a.vc.ps | a.vc.ts | a.vc.hs)) | (uintptr_t)a.D) & 15) != 0;
+    if (CT == W4A8_TYPE_E4M3 && apart)
+        launch3<CT, DP, CT == W4A8_TYPE_E4M3 ? kApart : kShort>(p, s);
+    else if (a.D != DP)
+        launch3<CT, DP, kShort>(p, s);
     else
-        launch3<CT, DP, false>(p, s);
+        launch3<CT, DP, kWhole>(p, s);
 }
 template <int CT>
 void launch1(const Plan& p, hipStream_t s)
 {
     if (p.pair)
-        launch3<CT, 128, false, true>(p, s);
+        launch3<CT, 128, kWhole, true>(p, s);
     else if (p.a.D <= 64)
         launch2<CT, 64>(p, s);
     else if (p.a.D <= 128)
