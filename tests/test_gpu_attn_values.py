@@ -1,0 +1,88 @@
+"""Values that decode attention has to get right beside the ordinary ones:
+infinite, far below the largest score, of the type's largest size."""
+import pytest
+import torch
+
+import attn_refs
+from test_gpu_attn import BF16, FP16, INF, dev, make_batch, near  # noqa: F401
+from w4a8_moe_grouped_amd import lib as w4
+
+pytestmark = pytest.mark.gpu
+
+
+def scored(dev, lens, kind, page=16, group=4, Hkv=2, D=64, extra=2, seed=0):
+    """A batch whose scores are set by each key's first element: q is 8 there and
+    0 elsewhere, keys are 0 in it, so with scale 1 a key's score is 8 times its
+    first element (exact in the cache's type)."""
+    d = make_batch(dev, lens, group * Hkv, Hkv, D, kind, page, extra=extra, seed=seed)
+    d["q"].zero_()
+    d["q"][..., 0] = 8.0
+    d["k_cache"][..., 0] = 0.0
+    return d
+
+
+def check(d, got, scale):
+    """Against the 64-bit form on the CPU (on the GPU torch's softmax of a long row makes 0 of e^-100 in 64 bits too)."""
+    host = {k: v if v is None else v.cpu() for k, v in d.items()}
+    want, err, lse, lse_err = attn_refs.attn_decode(
+        host["q"], host["k_cache"], host["v_cache"], host["page_table"], host["seq_lens"], scale=scale)
+    near(got[0].cpu(), want, err, d["q"].dtype)
+    near(got[1].cpu(), lse, lse_err, torch.float32)
+
+
+# uncut, cut over workgroups by the table's width, long, heads taken two by two
+FORMS = [dict(lens=[50, 3], extra=2), dict(lens=[50, 700], extra=3000), dict(lens=[20000], extra=0),
+         dict(lens=[70] * 130, Hkv=4), dict(lens=[400] * 16, extra=3000)]
+
+
+@pytest.mark.parametrize("kind", [BF16, FP16])
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("below", [0, 5, 12, 25, 40, 100, 250])
+def test_infinite_values_of_any_weight(dev, kind, page, below):  # noqa: F811
+    """An infinite value makes its element infinite however small its weight is (250 below: 2^-360, as a number of
+    64 bits still above 0); one of each sign makes it NaN; the other elements do not see it."""
+    for form in FORMS:
+        d = scored(dev, kind=kind, page=page, **form)
+        clean = w4.attn_decode(**d, scale=1.0)[0]
+        last = len(form["lens"]) - 1
+        n = form["lens"][last]
+        for j, h, e, v in ((0, 0, 5, INF), (n // 2, 1, 6, -INF), (n - 1, 0, 7, INF), (1, 1, 8, INF), (n - 2, 1, 8, -INF)):
+            d["k_cache"][d["page_table"][last, j // page].long(), j % page, :, 0] = -below / 8
+            d["v_cache"][d["page_table"][last, j // page].long(), j % page, h, e] = v
+        out, lse = w4.attn_decode(**d, scale=1.0, return_lse=True)
+        check(d, (out, lse), 1.0)
+        group = d["q"].shape[1] // d["k_cache"].shape[2]
+        assert bool((out[last, :group, 5] == INF).all()) and bool((out[last, group:2 * group, 6] == -INF).all())
+        assert bool((out[last, :group, 7] == INF).all())
+        both = out[last, group:2 * group, 8]
+        assert bool(torch.isnan(both).all() if n > 3 else (both == -INF).all())  # of 3 tokens they are the same
+        assert torch.equal(out[:last], clean[:last])
+
+
+@pytest.mark.parametrize("kind", [BF16, FP16])
+def test_infinite_values_before_the_maximum(dev, kind):  # noqa: F811
+    """Scores that rise by 200 behind an infinite value: what was summed before is scaled to nothing, but it stays infinite."""
+    for n, extra in ((300, 0), (6000, 0), (900, 3000)):
+        d = scored(dev, [n], kind, extra=extra)
+        j = torch.arange(n, device=dev)
+        rise = ((j * 4 // n) * 200.0 / 8).to(kind)  # four steps
+        d["k_cache"][d["page_table"][0, j // 16].long(), j % 16, :, 0] = rise[:, None]
+        d["v_cache"][d["page_table"][0, 0].long(), 2, 1, 9] = -INF
+        out, lse = w4.attn_decode(**d, scale=1.0, return_lse=True)
+        assert bool((out[0, 4:, 9] == -INF).all()) and int(torch.isfinite(out).sum()) == out.numel() - 4
+        check(d, (out, lse), 1.0)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP16])
+def test_infinite_values_under_a_score_of_minus_infinity(dev, kind):  # noqa: F811
+    """The definition's 0 times infinity: neither finite nor seen by another element."""
+    d = scored(dev, [40], kind)
+    page = d["page_table"][0, 0].long()
+    d["k_cache"][page, 3, :, 0] = -INF
+    clean = w4.attn_decode(**d, scale=1.0)[0]
+    d["v_cache"][page, 3, 0, 5] = INF
+    out = w4.attn_decode(**d, scale=1.0)[0]
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[0, :4, 5] = True
+    assert torch.equal(~torch.isfinite(out), bad)
+    near(out[~bad], clean[~bad].double(), torch.zeros((), dtype=torch.float64, device=dev).expand(int((~bad).sum())), kind)

@@ -135,10 +135,22 @@ __device__ __forceinline__ float exp2_(float x)
     return __builtin_amdgcn_exp2f(x);
 }
 
+// What sums are scaled by when their reference moves: above zero, so that an
+// infinite sum stays infinite
+__device__ __forceinline__ float factor(float x)
+{
+    return fmaxf(exp2_(x), 0x1p-120f);
+}
+
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+
 // The operand types of one kind of cache.  split: weights as a value cut to the
-// type and what the cut left, both above zero (zero times an infinite value
-// would be NaN).  fp16 holds the weights times 2^kShift: they stay below 2^(8 +
-// kShift), and the least part, 2^-24, is 2^-31 of the reference.
+// type and what the cut left.  Zero times an infinite value would be NaN, though a
+// weight is above zero however it rounds.  bf16 has the exponents to keep both
+// parts above zero (by 2^-110 of the reference and less); fp16 has not: its least
+// part, 2^-24 under weights that are held times 2^kShift (below 2^(8 + kShift)), is 2^-31 of the
+// reference, and `least` says whether parts are raised to it, 0x00010001, or not, 0.
+// e4m3 has no infinite values (and its weights, times the scales, any size).
 template <int CT>
 struct Kind;
 template <>
@@ -149,12 +161,16 @@ struct Kind<W4A8_TYPE_BF16> {
     }
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return f32x2_to_bf16x2(a, b); }
     static constexpr float kShift = 0.0f;
-    static __device__ __forceinline__ void split(float a, float b, int& hi, int& lo)
+    static __device__ __forceinline__ void split(float a, float b, uint32_t, int& hi, int& lo)
+    {
+        cut(fmaxf(a, 0x1p-110f), fmaxf(b, 0x1p-110f), 0x1p-118f, hi, lo);
+    }
+    static __device__ __forceinline__ void cut(float a, float b, float least, int& hi, int& lo)
     {
         hi = (int)__builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
         a -= __uint_as_float(__float_as_uint(a) & 0xFFFF0000u);
         b -= __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
-        lo = (int)pack(fmaxf(a, 0x1p-100f), fmaxf(b, 0x1p-100f));
+        lo = (int)pack(fmaxf(a, least), fmaxf(b, least));
     }
 };
 template <>
@@ -168,15 +184,25 @@ struct Kind<W4A8_TYPE_FP16> {
         return __builtin_bit_cast(uint32_t, v2h{(_Float16)a, (_Float16)b});
     }
     static constexpr float kShift = 7.0f;
-    static __device__ __forceinline__ void split(float a, float b, int& hi, int& lo)
+    static __device__ __forceinline__ void split(float a, float b, uint32_t least, int& hi, int& lo)
     {
         const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
-        hi = __builtin_bit_cast(int, h);
-        lo = (int)pack(fmaxf(a - (float)h[0], 0x1p-24f), fmaxf(b - (float)h[1], 0x1p-24f));
+        hi = raised(__builtin_bit_cast(uint32_t, h), least);
+        lo = raised(pack(a - (float)h[0], b - (float)h[1]), least);
+    }
+    // bits of values that are not negative order as the values do, NaN above all
+    static __device__ __forceinline__ int raised(uint32_t d, uint32_t least)
+    {
+        return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(v2us, d), __builtin_bit_cast(v2us, least)));
     }
 };
 template <>
-struct Kind<W4A8_TYPE_E4M3> : Kind<W4A8_TYPE_BF16> {};
+struct Kind<W4A8_TYPE_E4M3> : Kind<W4A8_TYPE_BF16> {
+    static __device__ __forceinline__ void split(float a, float b, uint32_t, int& hi, int& lo)
+    {
+        cut(a, b, 0.0f, hi, lo);  // under an infinite scale the rest is NaN and becomes 0
+    }
+};
 
 // two of a dword's four e4m3 codes -> two bf16 (exact)
 template <bool HIGH>
@@ -366,10 +392,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
             }
         }
         v4f o[kOut];
-#pragma unroll
-        for (int i = 0; i < kOut; ++i)
-            o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        float m = -__builtin_inff(), ref = -K::kShift, l = 0.0f;
+        float m, ref, l;
 
         const int first_kv = PAIR ? 2 * kv : kv, second = PAIR && c16 >= p.group / 2;  // which of a pair is this column's
         const char* const kbase = (const char*)a.kc.p + first_kv * a.kc.hs * kElem;
@@ -498,174 +521,192 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         // the segment's keys, in tiles that the waves take in turn
         constexpr int kStep = kTile * kWaves;
         const int seg0 = (start / kUnit + unit0) * kUnit, seg1 = min((start / kUnit + unit1) * kUnit, end);
-        int key0 = seg0 + wave * kTile;
-        while (key0 < seg1 && key0 + kTile <= start)
-            key0 += kStep;
-        Ids ids;
-        if (!CUT && RUNS && a.window == 0) {
-            // the first tile's place is known without the length: its pages are
-            // looked up while the length is on its way
-            auto early = [&](int key) {
-                const int id = table[min(page_of(p, key), a.max_pages - 1)];
-                return key < end ? held(id) : -1;
-            };
+        // fp16: a wave whose sums show NaN goes over its keys again with no part of a
+        // weight at zero, which leaves NaN where it belongs
+        for (uint32_t least = 0;; least = 0x00010001u) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                ids.k[n] = early(wave * kTile + 32 * n + krun);
-                ids.v[n] = early(wave * kTile + 32 * n + vrun);
-            }
-        } else {
-            ids = lookup_all(key0 < seg1 ? key0 : end);
-        }
-        if (key0 < seg1) {
-            load_k(key0, ids);
-            load_v(key0, ids);
-            if (key0 + kStep < seg1)
-                ids = lookup_all(key0 + kStep);
-        }
-        for (; key0 < seg1; key0 += kStep) {
-            const bool more = key0 + kStep < seg1;
-            v4f s[NT][2], s1[PAIR ? NT : 1][2];
+            for (int i = 0; i < kOut; ++i)
+                o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            m = -__builtin_inff(), ref = -K::kShift, l = 0.0f;
+            int key0 = seg0 + wave * kTile;
+            while (key0 < seg1 && key0 + kTile <= start)
+                key0 += kStep;
+            Ids ids;
+            if (!CUT && RUNS && a.window == 0) {
+                // the first tile's place is known without the length: its pages are
+                // looked up while the length is on its way
+                auto early = [&](int key) {
+                    const int id = table[min(page_of(p, key), a.max_pages - 1)];
+                    return key < end ? held(id) : -1;
+                };
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    s[n][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-                    if (PAIR)
-                        s1[PAIR ? n : 0][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int n = 0; n < NT; ++n) {
+                    ids.k[n] = early(wave * kTile + 32 * n + krun);
+                    ids.v[n] = early(wave * kTile + 32 * n + vrun);
                 }
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
+            } else {
+                ids = lookup_all(key0 < seg1 ? key0 : end);
+            }
+            if (key0 < seg1) {
+                load_k(key0, ids);
+                load_v(key0, ids);
+                if (key0 + kStep < seg1)
+                    ids = lookup_all(key0 + kStep);
+            }
+            for (; key0 < seg1; key0 += kStep) {
+                const bool more = key0 + kStep < seg1;
+                v4f s[NT][2], s1[PAIR ? NT : 1][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        v4i x;
-                        if (FP8) {
-                            const v4i& r = kreg[n][t][k >> 1];
-                            const uint32_t d0 = (uint32_t)r[2 * (k & 1)], d1 = (uint32_t)r[2 * (k & 1) + 1];
-                            x = v4i{(int)fp8x2_to_bf16<false>(d0), (int)fp8x2_to_bf16<true>(d0), (int)fp8x2_to_bf16<false>(d1),
-                                    (int)fp8x2_to_bf16<true>(d1)};
-                        } else {
-                            x = kreg[n][t][FP8 ? 0 : k];
-                        }
-                        v4f& sum = k < kQSteps ? s[n][t] : s1[PAIR ? n : 0][t];
-                        sum = K::mfma(x, q[k % kQSteps], sum);
+                        s[n][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+                        if (PAIR)
+                            s1[PAIR ? n : 0][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
                     }
-            Ids next = ids;
-            if (more) {
-                if (key0 + 2 * kStep < seg1)
-                    next = lookup_all(key0 + 2 * kStep);
-                load_k(key0 + kStep, ids);
-            }
-            // scores in powers of two; those that are not there are -inf
-            float x[NT][8];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[n][j] = (PAIR && second ? s1[PAIR ? n : 0][j >> 2][j & 3] : s[n][j >> 2][j & 3]) *
-                              (FP8 ? c * ksc[n][j] : c);
-            const bool whole = __all(mask == kAll);
-            if (!whole) {
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[n][j] = mask >> (8 * n + j) & 1 ? x[n][j] : -__builtin_inff();
-            }
-            float top = x[0][0];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    top = fmaxf(top, x[n][j]);
-            if (__any(top > m + 8.0f)) {
-                top = fmaxf(top, __shfl_xor(top, 16, 64));
-                top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const float high = fmaxf(m, top);
-                const float next_ref = high == -__builtin_inff() ? 0.0f : high;
-                const float f = exp2_(m - next_ref);
-                l *= f;
-#pragma unroll
-                for (int i = 0; i < kOut; ++i)
-                    o[i] *= f;
-                m = high;
-                ref = next_ref - K::kShift;
-            }
-            if (!whole) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (!(mask >> (8 * n + j) & 1)) {
-                            vsc[n][j] = 0.0f;
-#pragma unroll
-                            for (int h = 0; h < kHalves; ++h)
-                                vreg[n][j][h] = VChunk{};
+                        for (int t = 0; t < 2; ++t) {
+                            v4i x;
+                            if (FP8) {
+                                const v4i& r = kreg[n][t][k >> 1];
+                                const uint32_t d0 = (uint32_t)r[2 * (k & 1)], d1 = (uint32_t)r[2 * (k & 1) + 1];
+                                x = v4i{(int)fp8x2_to_bf16<false>(d0), (int)fp8x2_to_bf16<true>(d0), (int)fp8x2_to_bf16<false>(d1),
+                                        (int)fp8x2_to_bf16<true>(d1)};
+                            } else {
+                                x = kreg[n][t][FP8 ? 0 : k];
+                            }
+                            v4f& sum = k < kQSteps ? s[n][t] : s1[PAIR ? n : 0][t];
+                            sum = K::mfma(x, q[k % kQSteps], sum);
                         }
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                // the weights as a value of the type and the rest: the products'
-                // error is that of their sums (one rounding alone would add an
-                // error as large as the result's)
-                v4i ph, pl;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float w0 = exp2_(x[n][2 * j] - ref), w1 = exp2_(x[n][2 * j + 1] - ref);
-                    l += w0 + w1;
-                    if (FP8) {
-                        w0 *= vsc[n][2 * j];
-                        w1 *= vsc[n][2 * j + 1];
-                    }
-                    int hi, lo;
-                    K::split(w0, w1, hi, lo);
-                    ph[j] = hi;
-                    pl[j] = lo;
+                Ids next = ids;
+                if (more) {
+                    if (key0 + 2 * kStep < seg1)
+                        next = lookup_all(key0 + 2 * kStep);
+                    load_k(key0 + kStep, ids);
                 }
-                auto add = [&](int i, const v4i& e) {
-                    o[i] = K::mfma(e, ph, o[i]);
-                    o[i] = K::mfma(e, pl, o[i]);
-                };
+                // scores in powers of two; those that are not there are -inf
+                float x[NT][8];
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int d = 0; d < kVWords; ++d) {
-                        uint32_t word[8];
+                    for (int j = 0; j < 8; ++j)
+                        x[n][j] = (PAIR && second ? s1[PAIR ? n : 0][j >> 2][j & 3] : s[n][j >> 2][j & 3]) *
+                                  (FP8 ? c * ksc[n][j] : c);
+                const bool whole = __all(mask == kAll);
+                if (!whole) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            word[j] = ((const uint32_t*)&vreg[n][j][h])[d];
-                        if (!FP8) {  // two elements of eight keys
-                            v4i lo, hi;
+                            x[n][j] = mask >> (8 * n + j) & 1 ? x[n][j] : -__builtin_inff();
+                }
+                float top = x[0][0];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                lo[j] = (int)__builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x05040100u);
-                                hi[j] = (int)__builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x07060302u);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        top = fmaxf(top, x[n][j]);
+                if (__any(top > m + 8.0f)) {
+                    top = fmaxf(top, __shfl_xor(top, 16, 64));
+                    top = fmaxf(top, __shfl_xor(top, 32, 64));
+                    const float high = fmaxf(m, top);
+                    const float next_ref = high == -__builtin_inff() ? 0.0f : high;
+                    const float f = factor(m - next_ref);
+                    l *= f;
+#pragma unroll
+                    for (int i = 0; i < kOut; ++i)
+                        o[i] *= f;
+                    m = high;
+                    ref = next_ref - K::kShift;
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (!(mask >> (8 * n + j) & 1)) {
+                                vsc[n][j] = 0.0f;
+#pragma unroll
+                                for (int h = 0; h < kHalves; ++h)
+                                    vreg[n][j][h] = VChunk{};
                             }
-                            add(kPer * h + 2 * d, lo);
-                            add(kPer * h + 2 * d + 1, hi);
-                        } else {  // four elements of eight keys
-                            v4i e[4];
+                }
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t lo = __builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x05010400u);
-                                const uint32_t hi = __builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x07030602u);
-                                e[0][j] = (int)fp8x2_to_bf16<false>(lo);
-                                e[1][j] = (int)fp8x2_to_bf16<true>(lo);
-                                e[2][j] = (int)fp8x2_to_bf16<false>(hi);
-                                e[3][j] = (int)fp8x2_to_bf16<true>(hi);
-                            }
+                for (int n = 0; n < NT; ++n) {
+                    // the weights as a value of the type and the rest: the products'
+                    // error is that of their sums (one rounding alone would add an
+                    // error as large as the result's)
+                    v4i ph, pl;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                add(kPer * h + 4 * d + i, e[i]);
+                    for (int j = 0; j < 4; ++j) {
+                        float w0 = exp2_(x[n][2 * j] - ref), w1 = exp2_(x[n][2 * j + 1] - ref);
+                        l += w0 + w1;
+                        if (FP8) {
+                            w0 *= vsc[n][2 * j];
+                            w1 *= vsc[n][2 * j + 1];
                         }
+                        int hi, lo;
+                        K::split(w0, w1, least, hi, lo);
+                        ph[j] = hi;
+                        pl[j] = lo;
                     }
+                    auto add = [&](int i, const v4i& e) {
+                        o[i] = K::mfma(e, ph, o[i]);
+                        o[i] = K::mfma(e, pl, o[i]);
+                    };
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                        for (int d = 0; d < kVWords; ++d) {
+                            uint32_t word[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                word[j] = ((const uint32_t*)&vreg[n][j][h])[d];
+                            if (!FP8) {  // two elements of eight keys
+                                v4i lo, hi;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    lo[j] = (int)__builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x05040100u);
+                                    hi[j] = (int)__builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x07060302u);
+                                }
+                                add(kPer * h + 2 * d, lo);
+                                add(kPer * h + 2 * d + 1, hi);
+                            } else {  // four elements of eight keys
+                                v4i e[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t lo = __builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x05010400u);
+                                    const uint32_t hi = __builtin_amdgcn_perm(word[2 * j + 1], word[2 * j], 0x07030602u);
+                                    e[0][j] = (int)fp8x2_to_bf16<false>(lo);
+                                    e[1][j] = (int)fp8x2_to_bf16<true>(lo);
+                                    e[2][j] = (int)fp8x2_to_bf16<false>(hi);
+                                    e[3][j] = (int)fp8x2_to_bf16<true>(hi);
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    add(kPer * h + 4 * d + i, e[i]);
+                            }
+                        }
+                }
+                if (more) {
+                    load_v(key0 + kStep, ids);
+                    ids = next;
+                }
             }
-            if (more) {
-                load_v(key0 + kStep, ids);
-                ids = next;
-            }
+            if (CT != W4A8_TYPE_FP16 || least != 0)
+                break;
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < kOut; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; r += 2)
+                    nan |= __builtin_isunordered(o[i][r], o[i][r + 1]);
+            if (!__any(nan))
+                break;
         }
 
         // join the waves
@@ -689,7 +730,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         const float all_ref = all_m == -__builtin_inff() ? 0.0f : all_m;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            f[w] = exp2_(ml[w].x - (all_ref + K::kShift));
+            f[w] = factor(ml[w].x - (all_ref + K::kShift));
             all_l += ml[w].y * f[w];
         }
         const bool done = !CUT || (unit0 == 0 && unit1 == units);
@@ -771,7 +812,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(const Plan p
             float f = 0.0f;
             if (at + lane <= w1) {
                 const float2 ml = p.part_ml[slot_of(at + lane) + row];
-                f = exp2_(ml.x - ref);
+                f = factor(ml.x - ref);
                 l += ml.y * f;
             }
             const int n = min(64, w1 - at + 1);
