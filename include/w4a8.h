@@ -769,8 +769,10 @@ int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
  *                 with NULL: a function of B, q_heads, kv_heads, D, max_pages
  *                 and page_size)
  * Scores and sums are in fp32; a softmax weight meets the values as two parts of
- * q_type, whose sum is off by 2^-16 (bf16) or 2^-22 (fp16) of it.  Each result
- * is rounded once.  How a batch is cut follows all its lengths, so the order
+ * q_type, whose sum is off by 2^-16 (bf16) or 2^-22 (fp16) of it, or by 2^-80
+ * (bf16) or 2^-37 (fp16) of the row's largest weight where that is more.  An
+ * infinite value makes its element infinite however small its weight is.  Each
+ * result is rounded once.  How a batch is cut follows all its lengths, so the order
  * of a row's sums depends on the batch.
  * D = cache->head_dim: a multiple of 8 up to 256; q_heads a multiple of
  * kv_heads (INVALID_ARG otherwise); strides non-negative multiples of 8, B <=

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import attn_refs
+import attn_sharp
 from test_gpu_attn import BF16, FP16, INF, dev, make_batch, near  # noqa: F401
 from w4a8_moe_grouped_amd import lib as w4
 
@@ -86,3 +87,51 @@ def test_infinite_values_under_a_score_of_minus_infinity(dev, kind):  # noqa: F8
     bad[0, :4, 5] = True
     assert torch.equal(~torch.isfinite(out), bad)
     near(out[~bad], clean[~bad].double(), torch.zeros((), dtype=torch.float64, device=dev).expand(int((~bad).sum())), kind)
+
+
+# ---- weights -------------------------------------------------------------------------
+
+def check_sharp(d, **kw):
+    want, err = attn_sharp.attention(d["q"], d["k_cache"], d["v_cache"], d["page_table"], d["seq_lens"], d["k_scales"],
+                                     d["v_scales"], **kw)
+    out = w4.attn_decode(**d, **kw)[0]
+    torch.cuda.synchronize()
+    bad = attn_sharp.outside(out, want, err)
+    print("sharp", tuple(out.shape), d["k_cache"].dtype, "outside", bad, flush=True)
+    assert bad == 0
+
+
+@pytest.mark.parametrize("kind", [BF16, FP16])
+@pytest.mark.parametrize("above", [10, 15, 17, 20, 23])
+@pytest.mark.parametrize("peaks", [1, 16])
+def test_small_weights_under_peaks_of_no_value(dev, kind, above, peaks):  # noqa: F811
+    """Keys of unit variance below peaks whose values are 0: the output is theirs alone, in weights of e^-above and less."""
+    for form in (dict(lens=[4096], extra=0), dict(lens=[4096] * 70, Hkv=4, extra=0), dict(lens=[500], extra=0, page=100)):
+        d = scored(dev, kind=kind, **form)
+        n, page = form["lens"][0], d["k_cache"].shape[1]
+        g = torch.Generator(device=dev).manual_seed(above)
+        d["k_cache"][..., 0] = (torch.randn(d["k_cache"].shape[:3], generator=g, device=dev) / 8).to(kind)
+        d["v_cache"].copy_(1000 * (d["v_cache"].abs() + 0.5))
+        for b in range(len(form["lens"])):
+            j = torch.arange(peaks, device=dev) * (n // peaks) + 3
+            at = d["page_table"][b, j // page].long(), j % page
+            d["k_cache"][at[0], at[1], :, 0] = above / 8
+            d["v_cache"][at] = 0
+        check_sharp(d, scale=1.0)
+
+
+def test_very_many_small_weights(dev):  # noqa: F811
+    """2^20 keys of no weight to speak of, all of one value, and in each wave's share of them one that has all the weight.
+
+    The small ones are e^-30 of a large one and 8000 times its value: 512 to each add 4e-7.  What the format may
+    add is 2^-37 * 512 * 8000, 3e-5; sums of 512 keys and of 512 parts lose 2^-15 each: below half a step under 1, 2^-12."""
+    n = 1 << 20
+    d = scored(dev, [n], FP16, page=64, group=2, Hkv=1, extra=0)
+    d["k_cache"][..., 0] = -30 / 8
+    d["v_cache"].fill_(8000.0)
+    j = torch.arange(n, device=dev)
+    j = j[(j % 2048 < 128) & (j % 32 == 5)]
+    at = d["page_table"][0, j // 64].long(), j % 64
+    d["k_cache"][at[0], at[1], :, 0] = 0.0
+    d["v_cache"][at] = 1.0
+    assert bool((w4.attn_decode(**d, scale=1.0)[0] == 1.0).all())

@@ -16,7 +16,7 @@
 // registers, whole rows at a time, and LDS only joins the waves at the end.
 //
 // The maximum is taken lazily: sums are rescaled only when a score passes the
-// reference by 2^8, which a vote of the wave finds out.
+// reference by 2^8 (fp16: 2), which a vote of the wave finds out.
 //
 // Work: the batch's tiles are numbered (sequence, kv head, unit of 128 keys) and
 // cut evenly over the workgroups, from the lengths on the device.  A sequence
@@ -148,8 +148,10 @@ typedef unsigned short v2us __attribute__((ext_vector_type(2)));
 // type and what the cut left.  Zero times an infinite value would be NaN, though a
 // weight is above zero however it rounds.  bf16 has the exponents to keep both
 // parts above zero (by 2^-110 of the reference and less); fp16 has not: its least
-// part, 2^-24 under weights that are held times 2^kShift (below 2^(8 + kShift)), is 2^-31 of the
+// part, 2^-24 under weights that are held times 2^kShift, is 2^-38 of the
 // reference, and `least` says whether parts are raised to it, 0x00010001, or not, 0.
+// kLazy: the scores' lead over the reference, as a power of two, that moves it: weights
+// stay below 2^(kLazy + kShift), in fp16 2^15.
 // e4m3 has no infinite values (and its weights, times the scales, any size).
 template <int CT>
 struct Kind;
@@ -160,7 +162,7 @@ struct Kind<W4A8_TYPE_BF16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
     }
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return f32x2_to_bf16x2(a, b); }
-    static constexpr float kShift = 0.0f;
+    static constexpr float kShift = 0.0f, kLazy = 8.0f;
     static __device__ __forceinline__ void split(float a, float b, uint32_t, int& hi, int& lo)
     {
         cut(fmaxf(a, 0x1p-110f), fmaxf(b, 0x1p-110f), 0x1p-118f, hi, lo);
@@ -183,7 +185,7 @@ struct Kind<W4A8_TYPE_FP16> {
     {
         return __builtin_bit_cast(uint32_t, v2h{(_Float16)a, (_Float16)b});
     }
-    static constexpr float kShift = 7.0f;
+    static constexpr float kShift = 14.0f, kLazy = 1.0f;
     static __device__ __forceinline__ void split(float a, float b, uint32_t least, int& hi, int& lo)
     {
         const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
@@ -610,7 +612,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         top = fmaxf(top, x[n][j]);
-                if (__any(top > m + 8.0f)) {
+                if (__any(top > m + K::kLazy)) {
                     top = fmaxf(top, __shfl_xor(top, 16, 64));
                     top = fmaxf(top, __shfl_xor(top, 32, 64));
                     const float high = fmaxf(m, top);
