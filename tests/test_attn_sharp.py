@@ -1,5 +1,6 @@
 """The bounds of attn_sharp.py on the CPU: a weight's two parts meet them, and
 what they are there to see does not: one part alone, or parts that are raised."""
+import pytest
 import torch
 
 import attn_sharp
@@ -39,6 +40,16 @@ def misses(got, q, k, v, scale):
     table = torch.zeros(1, 1, dtype=torch.int32)
     want, err = attn_sharp.attention(q[None], k[None, :, None], v[None, :, None], table, torch.tensor([n]), scale=scale)
     return attn_sharp.outside(got[None], want, err)
+
+
+@pytest.mark.parametrize("dtype, shift", [(BF16, 0), (FP16, 14)])
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("n", [33, 128])
+def test_two_parts_are_within_and_one_is_not(dtype, shift, positive, n):
+    q, k, v = batch(dtype, n, positive)
+    assert misses(emulated(q, k, v, 0.125, shift, 2), q, k, v, 0.125) == 0
+    one = misses(emulated(q, k, v, 0.125, shift, 1), q, k, v, 0.125)
+    assert one > 100, one
 
 
 def test_parts_raised_for_every_key_are_seen():

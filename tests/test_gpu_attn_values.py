@@ -101,6 +101,23 @@ def check_sharp(d, **kw):
     assert bad == 0
 
 
+@pytest.mark.parametrize("kind", [BF16, FP16, "fp8"])
+@pytest.mark.parametrize("D", [64, 128, 256, 80])
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("positive", [False, True])
+def test_weights_have_two_parts(dev, kind, D, page, positive):  # noqa: F811
+    """Outputs are roundings of what the promised error allows; with a weight's second part
+    lost a quarter of them are not.  Queries of eight elements and few keys keep the other errors small."""
+    for extra in (0, 3000):
+        d = make_batch(dev, [128, 33, 100, 7, 128, 1], 8, 2, D, kind, page, extra=extra)
+        d["q"][..., 8:] = 0
+        if positive and kind == "fp8":
+            d["v_cache"] &= 0x7F
+        elif positive:
+            d["v_cache"].copy_(d["v_cache"].abs() + 0.5)
+        check_sharp(d)
+
+
 @pytest.mark.parametrize("kind", [BF16, FP16])
 @pytest.mark.parametrize("above", [10, 15, 17, 20, 23])
 @pytest.mark.parametrize("peaks", [1, 16])
