@@ -680,9 +680,9 @@ int w4a8_rope_frequencies(int64_t rotary_dim, double base, int scaling, double f
  * positions[t] * frequencies[i]:
  *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos)
  *   interleaved 0: a, b = elements i and i + R/2;  else 2i and 2i + 1
- * The other D - R elements are copied.  The angle is taken in 64 bits, its sine
- * and cosine are good to 2e-7 at any position, and every output is rounded
- * once from fp32.
+ * The other D - R elements are copied.  The angle is taken in twice 64 bits, its
+ * sine and cosine are good to 2e-7 at any position (times |magnitude|; for angles
+ * up to 2^80), and every output is rounded once from fp32.
  *   x, out        [T, heads, D] of `type` (fp32, bf16 or fp16), element (t, h, d) at
  *                 t * token_stride + h * head_stride + d; out may be x itself
  *                 (same strides) and does not overlap it otherwise

@@ -9,8 +9,8 @@
 // neighbouring lanes' chunks side by side; for pairs of halves a lane holds both
 // partners, so that no element crosses lanes.
 //
-// The angle's turns are reduced in 64 bits (at position 10^6 an fp32 angle is
-// off by 0.03), sine and cosine of what is left, at most an eighth of a turn,
+// The angle's turns are reduced in twice 64 bits (at position 10^6 an fp32 angle is
+// off by 0.03, at 2^31 one of 64 bits by more than sine and cosine are), sine and cosine of what is left, at most an eighth of a turn,
 // by their Taylor series in fp32.
 //
 // 16384 tokens x 40 heads of 128, fp32: 128 us (5.25 TB/s, a copy 5.1; with 32
@@ -28,12 +28,22 @@ constexpr int kWaves = 4;       // per workgroup
 constexpr int kMaxPairs = 128;  // D <= 256
 enum Layout { kPairs = 0, kHalves = 1, kHalvesAny = 2 };
 
-// cos and sin of 2 pi `turns`, times m
-__device__ __forceinline__ float2 cos_sin(double turns, float m)
+// cos and sin of the angle pos * f, times m.  The product and its turns are kept as
+// two numbers of 64 bits each, of which whole turns go first: one would be off by
+// 2^-53 of the angle, 2.4e-7 for each radian a position at position 2^31.
+__device__ __forceinline__ float2 cos_sin(double pos, double f, float m)
 {
+#pragma clang fp contract(off)  // turns - rint(turns) as one operation on the product would hold `rest` already
+    constexpr double kTurn = 0.15915494309189535, kTurnRest = -9.839338337591243e-18;  // 1 / (2 pi)
+    const double angle = pos * f, angle_rest = fma(pos, f, -angle);
+    double turns = angle * kTurn;
+    double rest = fma(angle, kTurn, -turns) + fma(angle, kTurnRest, angle_rest * kTurn);
+    turns -= rint(turns);
+    rest -= rint(rest);
+    turns += rest;
     const double quarter = rint(4.0 * turns);
     const float x = (float)((turns - 0.25 * quarter) * 6.283185307179586477);
-    const int n = (int)(quarter - 4.0 * floor(0.25 * quarter));
+    const int n = (int)quarter & 3;
     const float z = x * x;
     // |x| <= pi/4: the first terms left out are below 2e-9
     float s = fmaf(z, 1.0f / 362880, -1.0f / 5040);
@@ -144,10 +154,9 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
     if (a.kv_heads > 0)
         slot = a.slots[t];
     if (half > 0) {
-        const double turns_per = 0.15915494309189533577;
         const double pos = (double)a.positions[t];
         for (int i = lane; i < half; i += 64)
-            table[wave][i] = cos_sin(pos * a.frequencies[i] * turns_per, a.magnitude);
+            table[wave][i] = cos_sin(pos, a.frequencies[i], a.magnitude);
     }
     __builtin_amdgcn_wave_barrier();  // one wave: LDS operations stay in order
     const float2* cs = table[wave];
