@@ -703,7 +703,8 @@ int w4a8_rope(const void* x, int type, int64_t T, int64_t heads, int64_t head_di
  * k_token_stride + head * k_head_stride + d (elements; the same for v), so
  * both [pages, tokens, heads, D] and [pages, heads, tokens, D] serve, and
  * views of one buffer.  With type W4A8_TYPE_E4M3 the elements are codes and
- * each token and head has one positive fp32 scale, k_scales and v_scales
+ * each token and head has one fp32 scale between 2^-42 and 2^120 (as
+ * w4a8_kv_append writes them), k_scales and v_scales
  * [num_pages, kv_heads, page_size]; they are NULL for bf16 and fp16.  Codes
  * need no more than 8-byte alignment; strides are non-negative multiples of 8.
  * The struct itself is in host memory.
@@ -770,7 +771,8 @@ int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
  *                 and page_size)
  * Scores and sums are in fp32; a softmax weight meets the values as two parts of
  * q_type, whose sum is off by 2^-16 (bf16) or 2^-22 (fp16) of it, or by 2^-80
- * (bf16) or 2^-37 (fp16) of the row's largest weight where that is more.  An
+ * (bf16; with e4m3 values whose scales are at their least, 2^-46) or 2^-37 (fp16) of the row's
+ * largest weight where that is more.  An
  * infinite value makes its element infinite however small its weight is.  Each
  * result is rounded once.  How a batch is cut follows all its lengths, so the order
  * of a row's sums depends on the batch.

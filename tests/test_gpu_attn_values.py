@@ -152,3 +152,42 @@ def test_very_many_small_weights(dev):  # noqa: F811
     d["k_cache"][at[0], at[1], :, 0] = 0.0
     d["v_cache"][at] = 1.0
     assert bool((w4.attn_decode(**d, scale=1.0)[0] == 1.0).all())
+
+
+# ---- the largest values --------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", [BF16, FP16, "fp8"])
+@pytest.mark.parametrize("rise", [0, 1, 5, 30])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_largest_values(dev, kind, rise, mixed):  # noqa: F811
+    """Values of the type's largest size (e4m3: under the largest scale) have a mean of that size at most, under equal
+    scores and under scores that rise by `rise` nats every 32 keys."""
+    for lens, extra, Hkv in (([700, 40], 0, 2), ([20000], 0, 2), ([3000, 300], 3000, 2), ([300] * 130, 0, 4)):
+        d = scored(dev, lens, BF16 if kind == "fp8" else kind, extra=extra, Hkv=Hkv)
+        pages, page = d["k_cache"].shape[:2]
+        for b, n in enumerate(lens):
+            j = torch.arange(n, device=dev)
+            steps = (j // 32 % 12 * rise / 8).to(d["k_cache"].dtype)
+            d["k_cache"][d["page_table"][b, j // page].long(), j % page, :, 0] = steps[:, None]
+        sign = torch.where(d["v_cache"] > 0, 1.0, -1.0) if mixed else torch.ones_like(d["v_cache"])
+        most = torch.finfo(d["v_cache"].dtype).max
+        if kind == "fp8":
+            d["k_cache"] = d["k_cache"].to(torch.float8_e4m3fn).view(torch.uint8)
+            d["v_cache"] = (448 * sign).to(torch.float8_e4m3fn).view(torch.uint8)
+            d["k_scales"] = torch.ones(pages, Hkv, page, device=dev)
+            d["v_scales"] = torch.full((pages, Hkv, page), most / 448, device=dev)
+        else:
+            d["v_cache"] = (most * sign).to(d["v_cache"].dtype)
+        check_sharp(d, scale=1.0)
+        assert bool(torch.isfinite(w4.attn_decode(**d, scale=1.0)[0]).all())
+
+
+@pytest.mark.parametrize("least", ["all", "half"])
+def test_smallest_scales_of_codes(dev, least):  # noqa: F811
+    """Rows of (nearly) nothing, whose scales are the least that an append writes."""
+    for extra in (0, 3000):
+        d = make_batch(dev, [128, 33, 700, 1], 8, 2, 64, "fp8", 16, extra=extra)
+        d["q"][..., 8:] = 0
+        scales = d["v_scales"] if least == "all" else d["v_scales"][..., ::2]
+        scales.fill_(1e-10 / 448)
+        check_sharp(d)

@@ -147,11 +147,12 @@ typedef unsigned short v2us __attribute__((ext_vector_type(2)));
 // The operand types of one kind of cache.  split: weights as a value cut to the
 // type and what the cut left.  Zero times an infinite value would be NaN, though a
 // weight is above zero however it rounds.  bf16 has the exponents to keep both
-// parts above zero (by 2^-110 of the reference and less); fp16 has not: its least
-// part, 2^-24 under weights that are held times 2^kShift, is 2^-38 of the
-// reference, and `least` says whether parts are raised to it, 0x00010001, or not, 0.
+// parts above zero (2^-118 and 2^-126, under weights times 2^kShift 2^-80 of the
+// reference and less); fp16 has not: its least part, 2^-24, is 2^-38 of the reference, and
+// `least` says whether parts are raised to it, 0x00010001, or not, 0.
 // kLazy: the scores' lead over the reference, as a power of two, that moves it: weights
-// stay below 2^(kLazy + kShift), in fp16 2^15.
+// stay below 2^(kLazy + kShift), in fp16 2^15, else 2^-30: of 2^30 values of the type's
+// largest size the sum is finite.
 // e4m3 has no infinite values (and its weights, times the scales, any size).
 template <int CT>
 struct Kind;
@@ -162,10 +163,10 @@ struct Kind<W4A8_TYPE_BF16> {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b, a), __builtin_bit_cast(v8b, b), c, 0, 0, 0);
     }
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return f32x2_to_bf16x2(a, b); }
-    static constexpr float kShift = 0.0f, kLazy = 8.0f;
+    static constexpr float kShift = -38.0f, kLazy = 8.0f;
     static __device__ __forceinline__ void split(float a, float b, uint32_t, int& hi, int& lo)
     {
-        cut(fmaxf(a, 0x1p-110f), fmaxf(b, 0x1p-110f), 0x1p-118f, hi, lo);
+        cut(fmaxf(a, 0x1p-118f), fmaxf(b, 0x1p-118f), 0x1p-126f, hi, lo);
     }
     static __device__ __forceinline__ void cut(float a, float b, float least, int& hi, int& lo)
     {
@@ -205,6 +206,13 @@ struct Kind<W4A8_TYPE_E4M3> : Kind<W4A8_TYPE_BF16> {
         cut(a, b, 0.0f, hi, lo);  // under an infinite scale the rest is NaN and becomes 0
     }
 };
+
+// ln of a sum l of weights times 2^kShift, whose reference is m
+template <class K>
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return (m + __builtin_amdgcn_logf(__builtin_amdgcn_ldexpf(l, -(int)K::kShift))) * kLn2;
+}
 
 // two of a dword's four e4m3 codes -> two bf16 (exact)
 template <bool HIGH>
@@ -732,7 +740,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         const float all_ref = all_m == -__builtin_inff() ? 0.0f : all_m;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            f[w] = factor(ml[w].x - (all_ref + K::kShift));
+            f[w] = factor(ml[w].x - all_ref);
             all_l += ml[w].y * f[w];
         }
         const bool done = !CUT || (unit0 == 0 && unit1 == units);
@@ -768,7 +776,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
             if (!done)
                 p.part_ml[slot * kHeads + c16] = make_float2(all_m, all_l);
             else if (a.lse != nullptr)
-                a.lse[(int64_t)b * a.q_heads + head0 + c16] = (all_m + __builtin_amdgcn_logf(all_l)) * kLn2;
+                a.lse[(int64_t)b * a.q_heads + head0 + c16] = lse_of<K>(all_m, all_l);
         }
         __syncthreads();  // before the next segment writes into LDS
     }
@@ -862,7 +870,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(const Plan p
             if (lane + 64 * k < a.D)
                 out[lane + 64 * k] = (uint16_t)K::pack(y[k] * inv, 0.0f);
         if (lane == 0 && a.lse != nullptr)
-            a.lse[(int64_t)b * a.q_heads + head0 + row] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+            a.lse[(int64_t)b * a.q_heads + head0 + row] = lse_of<K>(m, l);
     }
 }
 
