@@ -525,7 +525,8 @@ int w4a8_norm_residual(const void* x, int x_type, int64_t ldx, const void* resid
  * w4a8_gemm_epilogue -- the dense W4AFP8 linear of w4a8_gemm with its
  * epilogue: out = bf16(act(A * W^T + bias) + residual), rounded once.  Of eight
  * consecutive products (k = 8i .. 8i + 7) the matrix instruction keeps each to
- * 2^-13 of the largest; their sums and all that follows are fp32.
+ * 2^-13 of the largest, for which it takes a subnormal activation code, one below
+ * 2^-6, as 2^-6; their sums and all that follows are fp32.
  *   a_e4m3, a_scales, b_int4, b_scales  as in w4a8_gemm; b has R rows, R = N,
  *                or R = 2N with W4A8_ACT_SWIGLU: gate rows [0, N), up rows
  *                [N, 2N), act = silu(gate) * up
@@ -637,9 +638,11 @@ int w4a8_fused_moe_stage_events(void* const* events, int n);
  * and up rows have blocks of their own), the block scales below 2^32 bytes and
  * each launch below 2^32 threads, which holds while ceil(M/16) * ceil(R/32) <
  * 2^23 - 8 (UNSUPPORTED otherwise); workspace query (0 bytes at present) and
- * errors as w4a8_gemm_epilogue.  A product is off by what the fp8 matrix instruction cuts (2^-13
- * of the largest of eight neighbours in K); sums over groups, scales and the
- * epilogue are in fp32, with one rounding at the end.
+ * errors as w4a8_gemm_epilogue.  Of eight consecutive products (k = 8i .. 8i + 7)
+ * the matrix instruction keeps each to 2^-13 of the largest, for which it takes a
+ * subnormal code, one below 2^-6, as 2^-6; sums over groups, scales and the
+ * epilogue are in fp32, with one rounding at the end.  a_scale * b_scale is
+ * formed first and has to be finite.
  */
 int w4a8_gemm_fp8(const uint8_t* a_e4m3, const float* a_scales, int64_t M, int64_t K,
                   const uint8_t* b_e4m3, const float* b_scales, int64_t N, const void* bias,
