@@ -1,8 +1,10 @@
 // attn_decode.hip -- attention of one new token per sequence over the paged
 // cache (w4a8_attn_decode).
 //
-// Bound by the cache's bytes, each read once for all the query heads of its kv
-// head.  A wave takes tiles of 32 keys and keeps everything in registers:
+// Bound by the cache's bytes, each read once for up to 16 query heads of its kv
+// head (each 16 more read them again: 64 x 4096 keys, one kv head of 128, bf16,
+// 16 query heads 32 us, 32 52, 128 152).  A wave takes tiles of 32 keys and keeps
+// everything in registers:
 //   S[key, head] = K Q^T and O[d, head] += V^T P^T are MFMA 16x16x32 with the
 //   heads (up to 16) as columns, so a lane holds one head's scores and sums
 //   and the softmax needs no exchange but the maximum's.
@@ -25,10 +27,10 @@
 // one is finished there.  Where sequences are short by the table or the window (`cuts`),
 // a workgroup takes one sequence and kv head whole, and there is no second launch.
 //
-// 64 x 4096 keys, 64 / 8 heads of 128, bf16: 193 us (5.6 TB/s; a reduction reads
+// 64 x 4096 keys, 64 / 8 heads of 128, bf16: 195 us (5.5 TB/s; a reduction reads
 // 6.1) and 4.7 for the second launch, which finds nothing to join; 655 MB of e4m3
-// in 16 sequences: 135 + 6.5 (rows of 128 bytes, 1 KB apart); one sequence of
-// 1000: 7.9 + 4.6.
+// in 16 sequences: 137 + 6.8 (rows of 128 bytes, 1 KB apart); one sequence of
+// 1000: 7.8 + 4.7.
 #include "api_util.hpp"
 #include "common.hpp"
 #include "internal.hpp"
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         VChunk vreg[NT][8][kHalves];
         float ksc[NT][8], vsc[NT][8];
         uint32_t mask = 0;  // which of the lane's keys 32 n + 8 g + j of the tile are there, bit 8 n + j
-        constexpr uint32_t kAll = NT == 4 ? 0xFFFFFFFFu : (1u << (8 * NT & 31)) - 1;
+        constexpr uint32_t kAll = (1u << 8 * NT) - 1;
 
         // the page of key `key`, or of the run of keys from `key`; -1: nothing of it is seen
         auto held = [&](int id) { return id >= 0 && id < a.num_pages ? id : -1; };
