@@ -771,14 +771,16 @@ int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
  *   lse           [B, q_heads] fp32, or NULL
  *   workspace     partial results of sequences that are cut into parts (query
  *                 with NULL: a function of B, q_heads, kv_heads, D, max_pages
- *                 and page_size)
+ *                 and page_size).  Calls that may run at once, replays of
+ *                 captured graphs among them, need one each
  * Scores and sums are in fp32; a softmax weight meets the values as two parts of
- * q_type, whose sum is off by 2^-16 (bf16) or 2^-22 (fp16) of it, or by 2^-80
- * (bf16; with e4m3 values whose scales are at their least, 2^-46) or 2^-37 (fp16) of the row's
- * largest weight where that is more.  An
- * infinite value makes its element infinite however small its weight is.  Each
- * result is rounded once.  How a batch is cut follows all its lengths, so the order
- * of a row's sums depends on the batch.
+ * q_type, whose sum is off by 2^-16 (bf16) or 2^-22 (fp16) of it, or, where that is
+ * more, by 2^-80 (bf16; with e4m3 values whose scales are at their least, 2^-46)
+ * or 2^-37 (fp16) of the row's largest weight.  Values of the type's largest size
+ * do not overflow.  An infinite value makes its element infinite however small its
+ * weight is; a score of +infinity or NaN makes its row NaN, the lse too; scores of
+ * -infinity weigh nothing.  Each result is rounded once.  How a batch is cut follows
+ * all its lengths, so the order of a row's sums depends on the batch.
  * D = cache->head_dim: a multiple of 8 up to 256; q_heads a multiple of
  * kv_heads (INVALID_ARG otherwise); strides non-negative multiples of 8, B <=
  * 65536, q_heads <= 4096, B * kv_heads * ceil(q_heads / kv_heads / 16) <= 2^22,

@@ -191,3 +191,22 @@ def test_smallest_scales_of_codes(dev, least):  # noqa: F811
         scales = d["v_scales"] if least == "all" else d["v_scales"][..., ::2]
         scales.fill_(1e-10 / 448)
         check_sharp(d)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP16])
+@pytest.mark.parametrize("extra", [0, 3000])
+def test_infinite_scores(dev, kind, extra):  # noqa: F811
+    """+infinity and NaN make their rows NaN, -infinity weighs nothing, and a row of nothing else is 0."""
+    d = scored(dev, [70, 70, 70, 70, 600], kind, extra=extra)
+    clean = w4.attn_decode(**d, scale=1.0, return_lse=True)
+    for b, value, tokens in ((0, INF, [33]), (1, float("nan"), [69]), (2, -INF, [0, 5, 64]), (3, -INF, list(range(70)))):
+        for j in tokens:
+            d["k_cache"][d["page_table"][b, j // 16].long(), j % 16, 0, 0] = value  # of the first kv head
+    out, lse = w4.attn_decode(**d, scale=1.0, return_lse=True)
+    assert bool(torch.isnan(out[:2, :4]).all()) and bool(torch.isnan(lse[:2, :4]).all())
+    assert bool((out[3, :4] == 0).all()) and bool((lse[3, :4] == -INF).all())
+    near(lse[2, :4], torch.full((4,), 67.0, dtype=torch.float64, device=dev).log(),
+         torch.full((4,), 1e-5, dtype=torch.float64, device=dev))
+    assert bool(torch.isfinite(out[2]).all())
+    for got, want in zip((out, lse), clean):
+        assert torch.equal(got[:, 4:], want[:, 4:]) and torch.equal(got[4], want[4])
