@@ -11,7 +11,7 @@
 // rows), so the product of scales is a single multiplication for 16 rows.
 //
 // Few rows (fp8_rows_kernel): bound by the weight bytes and by latency.  1 x 7168 x
-// 10240: 13.8 us (5.3 TB/s); 64 x 8192 x 7168: 13.7 (4.5 TB/s); 333 x 1664 x 2050: 7.6.
+// 10240: 13.8 us (5.3 TB/s); 64 x 8192 x 7168: 13.7 (4.4 TB/s); 333 x 1664 x 2050: 7.6.
 // Many (fp8_tile_kernel): by the matrix unit, the promotion beside it and power.
 // 4096 x 7168 x 8192: 228 to 258 us by the box (1.9 to 2.1 PFLOP/s; the matrix
 // unit busy 53% of the cycles, other vector instructions 44%), with operands of zero 180;

@@ -13,9 +13,11 @@
 // off by 0.03, at 2^31 one of 64 bits by more than sine and cosine are), sine and cosine of what is left, at most an eighth of a turn,
 // by their Taylor series in fp32.
 //
-// 16384 tokens x 40 heads of 128, fp32: 128 us (5.25 TB/s, a copy 5.1; with 32
+// 16384 tokens x 40 heads of 128, fp32: 127 us (5.3 TB/s, a copy 5.1; with 32
 // contiguous bytes a lane 154); append of 16384 tokens, 64 + 2 x 8 heads, to
-// e4m3: 126 us (5.1 TB/s); 64 tokens: 4.0 and 4.5 us, two memory latencies.
+// e4m3: 124 us (5.1 TB/s); 64 tokens: 3.6 and 4.4 us, two memory latencies.
+// Halves that are no whole chunks read partners one by one (16384 x 72 x 80, bf16,
+// 20 of it turned: 144 us, interleaved 77).
 #include "common.hpp"
 #include "internal.hpp"
 #include "w4a8.h"
