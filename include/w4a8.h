@@ -775,8 +775,8 @@ int w4a8_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
  *                 captured graphs among them, need one each
  * Scores and sums are in fp32; a softmax weight meets the values as two parts of
  * q_type, whose sum is off by 2^-16 (bf16) or 2^-22 (fp16) of it, or, where that is
- * more, by 2^-80 (bf16; with e4m3 values whose scales are at their least, 2^-46)
- * or 2^-37 (fp16) of the row's largest weight.  Values of the type's largest size
+ * more, by 2^-88 (bf16; with e4m3 values whose scales are at their least, 2^-46)
+ * or 2^-38 (fp16) of the row's largest weight.  Values of the type's largest size
  * do not overflow.  An infinite value makes its element infinite however small its
  * weight is; a score of +infinity or NaN makes its row NaN, the lse too; scores of
  * -infinity weigh nothing.  Each result is rounded once.  How a batch is cut follows

@@ -7,7 +7,7 @@ from attn_refs import U, gather
 
 # a weight, as its two parts: off by PART of it, or by LEAST of the row's largest weight
 PART = {torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -22}
-LEAST = {torch.bfloat16: 2.0 ** -80, torch.float16: 2.0 ** -37}
+LEAST = {torch.bfloat16: 2.0 ** -88, torch.float16: 2.0 ** -38}
 
 
 def attention(q, k_cache, v_cache, table, lens, k_scales=None, v_scales=None, scale=None, window=0):

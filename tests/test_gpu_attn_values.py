@@ -210,3 +210,38 @@ def test_infinite_scores(dev, kind, extra):  # noqa: F811
     assert bool(torch.isfinite(out[2]).all())
     for got, want in zip((out, lse), clean):
         assert torch.equal(got[:, 4:], want[:, 4:]) and torch.equal(got[4], want[4])
+
+
+@pytest.mark.parametrize("kind", [BF16, FP16])
+@pytest.mark.parametrize("value", [INF, float("nan"), "largest"])
+@pytest.mark.parametrize("below", [8, 60, 110, 400, INF])
+def test_values_that_are_far_off_stay_where_they_are(dev, kind, value, below):  # noqa: F811
+    """One element of one key that is infinite, NaN or of the type's largest size: no other element, head or sequence
+    changes by a bit; and the largest adds no more than its weight has it (nothing, where that is below 2^-150)."""
+    for form in FORMS:
+        d = scored(dev, kind=kind, **form)
+        last = len(form["lens"]) - 1
+        n = form["lens"][last]
+        places = [(j, h, 3 + 7 * i) for i, (j, h) in enumerate(((0, 0), (n // 2, 1), (n - 1, 0)))]
+        for j, h, e in places:
+            at = d["page_table"][last, j // 16].long(), j % 16
+            d["k_cache"][at[0], at[1], :, 0] = -below / 8
+            d["v_cache"][at[0], at[1], h, e] = 0.0
+        clean = w4.attn_decode(**d, scale=1.0, return_lse=True)
+        assert bool(torch.isfinite(clean[0]).all())
+        for j, h, e in places:
+            d["v_cache"][d["page_table"][last, j // 16].long(), j % 16, h, e] = (
+                torch.finfo(kind).max if value == "largest" else value)
+        out, lse = w4.attn_decode(**d, scale=1.0, return_lse=True)
+        assert torch.equal(lse, clean[1])
+        group = d["q"].shape[1] // d["k_cache"].shape[2]
+        changed = torch.zeros_like(out, dtype=torch.bool)
+        for j, h, e in places:
+            changed[last, h * group:(h + 1) * group, e] = True
+        if value == "largest" and below > 104 and (n > 3 or below == INF):  # of three tokens all are so far below
+            changed[:] = False
+        assert torch.equal(out[~changed], clean[0][~changed])
+        if value != "largest":
+            assert not bool(torch.isfinite(out[changed]).any())
+        elif changed.any():
+            check(d, (out, lse), 1.0)

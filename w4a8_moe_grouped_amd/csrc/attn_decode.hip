@@ -137,25 +137,36 @@ __device__ __forceinline__ float exp2_(float x)
     return __builtin_amdgcn_exp2f(x);
 }
 
-// What sums are scaled by when their reference moves: above zero, so that an
-// infinite sum stays infinite
-__device__ __forceinline__ float factor(float x)
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+// whether one of n numbers is NaN (or infinite), without a comparison for each (their
+// results go through scalar registers: 0.2 us at the end of a wave's keys)
+template <int N>
+__device__ __forceinline__ bool not_finite(const float (&x)[N])
 {
-    return fmaxf(exp2_(x), 0x1p-120f);
+    float zero[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        zero[i & 1] = fmaf(x[i], 0.0f, zero[i & 1]);
+    return zero[0] != zero[1];
+}
+// two 16-bit values, not negative, each not below its half of `least`: their bits
+// order as they do, NaN above all
+__device__ __forceinline__ int raised(uint32_t d, uint32_t least)
+{
+    return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(v2us, d), __builtin_bit_cast(v2us, least)));
 }
 
-typedef unsigned short v2us __attribute__((ext_vector_type(2)));
-
 // The operand types of one kind of cache.  split: weights as a value cut to the
-// type and what the cut left.  Zero times an infinite value would be NaN, though a
-// weight is above zero however it rounds.  bf16 has the exponents to keep both
-// parts above zero (2^-118 and 2^-126, under weights times 2^kShift 2^-80 of the
-// reference and less); fp16 has not: its least part, 2^-24, is 2^-38 of the reference, and
-// `least` says whether parts are raised to it, 0x00010001, or not, 0.
-// kLazy: the scores' lead over the reference, as a power of two, that moves it: weights
-// stay below 2^(kLazy + kShift), in fp16 2^15, else 2^-30: of 2^30 values of the type's
-// largest size the sum is finite.
-// e4m3 has no infinite values (and its weights, times the scales, any size).
+// type and what the cut left, each not below `least` (two of them in its halves).
+// The weights are held times 2^kShift.  kLazy: the scores' lead over the reference, as a
+// power of two, that moves it: weights stay below 2^(kLazy + kShift).  fp16, whose
+// least part is 2^-24, holds them as large as it can, below 2^15; else they stay
+// below 2^-30: of 2^30 values of the type's largest size the sum is finite.
+// Zero times an infinite value is NaN, though a weight is above zero however it
+// rounds.  So a wave (of a 16-bit cache; e4m3 has no infinity) whose sums show NaN goes
+// over its keys again with no part below kLeast and no sum scaled by less than
+// kLeastFactor, and takes from that what was NaN; sums without it see nothing of it.
+constexpr float kLeastFactor = 0x1p-120f;
 template <int CT>
 struct Kind;
 template <>
@@ -166,16 +177,19 @@ struct Kind<W4A8_TYPE_BF16> {
     }
     static __device__ __forceinline__ uint32_t pack(float a, float b) { return f32x2_to_bf16x2(a, b); }
     static constexpr float kShift = -38.0f, kLazy = 8.0f;
-    static __device__ __forceinline__ void split(float a, float b, uint32_t, int& hi, int& lo)
+    static constexpr uint32_t kLeast = 0x00800080;  // 2^-126
+    static __device__ __forceinline__ void split(float a, float b, uint32_t least, int& hi, int& lo)
     {
-        cut(fmaxf(a, 0x1p-118f), fmaxf(b, 0x1p-118f), 0x1p-126f, hi, lo);
+        hi = raised(cut(a, b), least);
+        lo = raised(pack(a, b), least);
     }
-    static __device__ __forceinline__ void cut(float a, float b, float least, int& hi, int& lo)
+    // the values cut to the type; a and b become the rest
+    static __device__ __forceinline__ uint32_t cut(float& a, float& b)
     {
-        hi = (int)__builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+        const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
         a -= __uint_as_float(__float_as_uint(a) & 0xFFFF0000u);
         b -= __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
-        lo = (int)pack(fmaxf(a, least), fmaxf(b, least));
+        return hi;
     }
 };
 template <>
@@ -189,23 +203,20 @@ struct Kind<W4A8_TYPE_FP16> {
         return __builtin_bit_cast(uint32_t, v2h{(_Float16)a, (_Float16)b});
     }
     static constexpr float kShift = 14.0f, kLazy = 1.0f;
+    static constexpr uint32_t kLeast = 0x00010001;  // 2^-24
     static __device__ __forceinline__ void split(float a, float b, uint32_t least, int& hi, int& lo)
     {
         const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
         hi = raised(__builtin_bit_cast(uint32_t, h), least);
         lo = raised(pack(a - (float)h[0], b - (float)h[1]), least);
     }
-    // bits of values that are not negative order as the values do, NaN above all
-    static __device__ __forceinline__ int raised(uint32_t d, uint32_t least)
-    {
-        return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(v2us, d), __builtin_bit_cast(v2us, least)));
-    }
 };
 template <>
 struct Kind<W4A8_TYPE_E4M3> : Kind<W4A8_TYPE_BF16> {
     static __device__ __forceinline__ void split(float a, float b, uint32_t, int& hi, int& lo)
     {
-        cut(a, b, 0.0f, hi, lo);  // under an infinite scale the rest is NaN and becomes 0
+        hi = (int)cut(a, b);
+        lo = (int)pack(fmaxf(a, 0.0f), fmaxf(b, 0.0f));  // under an infinite scale the rest is NaN
     }
 };
 
@@ -533,9 +544,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         // the segment's keys, in tiles that the waves take in turn
         constexpr int kStep = kTile * kWaves;
         const int seg0 = (start / kUnit + unit0) * kUnit, seg1 = min((start / kUnit + unit1) * kUnit, end);
-        // fp16: a wave whose sums show NaN goes over its keys again with no part of a
-        // weight at zero, which leaves NaN where it belongs
-        for (uint32_t least = 0;; least = 0x00010001u) {
+        for (uint32_t least = 0;; least = K::kLeast) {
 #pragma unroll
             for (int i = 0; i < kOut; ++i)
                 o[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -627,7 +636,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                     top = fmaxf(top, __shfl_xor(top, 32, 64));
                     const float high = fmaxf(m, top);
                     const float next_ref = high == -__builtin_inff() ? 0.0f : high;
-                    const float f = factor(m - next_ref);
+                    const float f = fmaxf(exp2_(m - next_ref), least != 0 ? kLeastFactor : 0.0f);
                     l *= f;
 #pragma unroll
                     for (int i = 0; i < kOut; ++i)
@@ -709,16 +718,34 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
                     ids = next;
                 }
             }
-            if (CT != W4A8_TYPE_FP16 || least != 0)
+            if (FP8)
                 break;
-            bool nan = false;
+            // the wave's own part of LDS holds the first sums meanwhile
+            if (__builtin_expect(least != 0, 0)) {
+#pragma unroll
+                for (int i = 0; i < kOut; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float first = sh_o[wave][4 * i + r][lane];
+                        o[i][r] = first != first ? o[i][r] : first;
+                    }
+                break;
+            }
+            bool odd = false;
+            {
+                float all[4 * kOut];
+#pragma unroll
+                for (int i = 0; i < 4 * kOut; ++i)
+                    all[i] = o[i >> 2][i & 3];
+                odd = not_finite(all);
+            }
+            if (__builtin_expect(!__any(odd), 1))
+                break;
 #pragma unroll
             for (int i = 0; i < kOut; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; r += 2)
-                    nan |= __builtin_isunordered(o[i][r], o[i][r + 1]);
-            if (!__any(nan))
-                break;
+                for (int r = 0; r < 4; ++r)
+                    sh_o[wave][4 * i + r][lane] = o[i][r];
         }
 
         // join the waves
@@ -742,7 +769,7 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         const float all_ref = all_m == -__builtin_inff() ? 0.0f : all_m;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            f[w] = factor(ml[w].x - all_ref);
+            f[w] = exp2_(ml[w].x - all_ref);
             all_l += ml[w].y * f[w];
         }
         const bool done = !CUT || (unit0 == 0 && unit1 == units);
@@ -752,12 +779,20 @@ __global__ __launch_bounds__(64 * waves_of(DP, CUT), DP == 256 ? 1 : 2) void att
         for (int it = wave; it < 4 * kHalves; it += kWaves) {
             const int r = it & 3, h = it >> 2;
             float y[kPer];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                y[i] = 0.0f;
+            auto joined = [&](int i, float least) {
+                float sum = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWaves; ++w)
-                    y[i] += sh_o[w][4 * (kPer * h + i) + r][lane] * f[w];
+                    sum += sh_o[w][4 * (kPer * h + i) + r][lane] * fmaxf(f[w], least);
+                return sum;
+            };
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                y[i] = joined(i, 0.0f);
+            if (!FP8 && __builtin_expect(__any(not_finite(y)), 0)) {  // perhaps an infinite sum times 0
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    y[i] = y[i] != y[i] ? joined(i, kLeastFactor) : y[i];
             }
             const int row_d = 128 * h + kPer * (4 * g + r), d = PAIR ? row_d & 63 : row_d;
             if (c16 < heads && (PAIR ? row_d >> 6 == second : d < a.D)) {
@@ -815,39 +850,55 @@ __global__ __launch_bounds__(64 * kJoinWaves) void attn_join_kernel(const Plan p
     auto slot_of = [&](int w) { return (2 * (int64_t)w + (w == w0 ? later : 0)) * kHeads; };
     const int first = (int)((int64_t)blockIdx.x - id * parts) * ROWS + (ROWS == 1 ? 0 : wave);
     for (int row = first; row < heads && row < first + ROWS; row += ROWS == 1 ? 1 : kJoinWaves) {
-        float m = -__builtin_inff(), l = 0.0f, y[kMost] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float m = -__builtin_inff(), l, y[kMost];
         for (int w = w0 + lane; w <= w1; w += 64)
             m = fmaxf(m, p.part_ml[slot_of(w) + row].x);
         m = group_max<64>(m);
         const float ref = m == -__builtin_inff() ? 0.0f : m;
-        for (int at = w0; at <= w1; at += 64) {
-            float f = 0.0f;
-            if (at + lane <= w1) {
-                const float2 ml = p.part_ml[slot_of(at + lane) + row];
-                f = factor(ml.x - ref);
-                l += ml.y * f;
-            }
-            const int n = min(64, w1 - at + 1);
-            for (int i0 = ROWS == 1 ? wave : 0; i0 < n; i0 += 4 * kSplit) {
-                float v[4][kMost];
+        // the parts' sums, each times its factor, but no less than `least`
+        auto sums = [&](float least, float (&sum)[kMost]) {
+            l = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float* src = p.part_o + (slot_of(at + min(i0 + j * kSplit, n - 1)) + row) * a.D;
-#pragma unroll
-                    for (int k = 0; k < kMost; ++k)
-                        v[j][k] = lane + 64 * k < a.D ? src[lane + 64 * k] : 0.0f;
+            for (int k = 0; k < kMost; ++k)
+                sum[k] = 0.0f;
+            for (int at = w0; at <= w1; at += 64) {
+                float f = 0.0f;
+                if (at + lane <= w1) {
+                    const float2 ml = p.part_ml[slot_of(at + lane) + row];
+                    f = exp2_(ml.x - ref);
+                    l += ml.y * f;
+                    f = fmaxf(f, least);
                 }
+                const int n = min(64, w1 - at + 1);
+                for (int i0 = ROWS == 1 ? wave : 0; i0 < n; i0 += 4 * kSplit) {
+                    float v[4][kMost];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = i0 + j * kSplit;
-                    if (i < n) {
-                        const float g = __shfl(f, i, 64);
+                    for (int j = 0; j < 4; ++j) {
+                        const float* src = p.part_o + (slot_of(at + min(i0 + j * kSplit, n - 1)) + row) * a.D;
 #pragma unroll
                         for (int k = 0; k < kMost; ++k)
-                            y[k] = fmaf(v[j][k], g, y[k]);
+                            v[j][k] = lane + 64 * k < a.D ? src[lane + 64 * k] : 0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = i0 + j * kSplit;
+                        if (i < n) {
+                            const float g = __shfl(f, i, 64);
+#pragma unroll
+                            for (int k = 0; k < kMost; ++k)
+                                sum[k] = fmaf(v[j][k], g, sum[k]);
+                        }
                     }
                 }
             }
+        };
+        sums(0.0f, y);
+        if (__builtin_expect(__any(not_finite(y)), 0)) {  // perhaps an infinite sum times 0
+            float z[kMost];
+            sums(kLeastFactor, z);
+#pragma unroll
+            for (int k = 0; k < kMost; ++k)
+                y[k] = y[k] != y[k] ? z[k] : y[k];
         }
         l = group_sum<64>(l);
         if (ROWS == 1) {
