@@ -707,7 +707,7 @@ int w4a8_rope(const void* x, int type, int64_t T, int64_t heads, int64_t head_di
  * both [pages, tokens, heads, D] and [pages, heads, tokens, D] serve, and
  * views of one buffer.  With type W4A8_TYPE_E4M3 the elements are codes and
  * each token and head has one fp32 scale between 2^-42 and 2^120 (as
- * w4a8_kv_append writes them), k_scales and v_scales
+ * w4a8_kv_append writes them, where all is finite), k_scales and v_scales
  * [num_pages, kv_heads, page_size]; they are NULL for bf16 and fp16.  Codes
  * need no more than 8-byte alignment; strides are non-negative multiples of 8.
  * The struct itself is in host memory.
@@ -741,7 +741,8 @@ typedef struct {
  *                 (positions may be NULL with rotary_dim 0)
  * e4m3: the D elements of a head, rotated and not rounded before, are one
  * block of the quantisation rule above: scale = max(amax, 1e-10) / 448, code =
- * e4m3(clamp(x * 448 / max(amax, 1e-10))); a NaN shows in the scale.  All
+ * e4m3(clamp(x * 448 / max(amax, 1e-10))); a NaN makes the scale NaN and an
+ * infinity makes it infinite, and both have the code NaN.  All
  * else in the cache stays as it was.
  * D = cache->head_dim; strides are non-negative multiples of 8, and rows that
  * are written lie apart (no stride of 0 along more than one); sizes and errors as w4a8_rope, and q_heads + 2 * kv_heads <= 4096.  slots is 8-byte aligned.

@@ -245,3 +245,34 @@ def test_values_that_are_far_off_stay_where_they_are(dev, kind, value, below):  
             assert not bool(torch.isfinite(out[changed]).any())
         elif changed.any():
             check(d, (out, lse), 1.0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 200])
+@pytest.mark.parametrize("R", [0, 32])
+def test_infinite_elements_in_an_appended_row_of_codes(dev, D, R):  # noqa: F811
+    """By the rule an infinity's row has an infinite scale, its own code is that of infinity times 0, NaN, and the
+    others' are 0: what attends to the row is NaN, whatever signs meet (an infinite key was passed over where its
+    score came out as -infinity)."""
+    T, H = 40, 2
+    g = torch.Generator(device=dev).manual_seed(D)
+    x = torch.randn(T, 2 * H, D, generator=g, device=dev).to(BF16)
+    k, v = x[:, :H], x[:, H:]
+    k[3, 0, 40], k[20, 1, 41], v[30, 0, 42] = INF, -INF, INF  # not among those that are turned
+    kc, vc = (torch.zeros(3, 16, H, D, dtype=torch.uint8, device=dev) for _ in range(2))
+    ks, vs = (torch.zeros(3, H, 16, device=dev) for _ in range(2))
+    kw = dict(positions=torch.arange(T, dtype=torch.int32, device=dev), frequencies=w4.rope_frequencies(R, device=dev)) if R else {}
+    w4.kv_append(k, v, kc, vc, torch.arange(T, device=dev), k_scales=ks, v_scales=vs, **kw)
+    for cache, scales, j, h, e in ((kc, ks, 3, 0, 40), (kc, ks, 20, 1, 41), (vc, vs, 30, 0, 42)):
+        row = cache.view(-1, H, D)[j, h].clone()
+        assert float(scales[j // 16, h, j % 16]) == INF and int(row[e]) & 0x7F == 0x7F
+        row[e] = 0
+        assert bool((row & 0x7F == 0).all())
+    assert int(torch.isfinite(ks).sum()) == ks.numel() - 2 and int(torch.isfinite(vs).sum()) == vs.numel() - 1
+    table = torch.arange(3, dtype=torch.int32, device=dev).expand(4, 3).contiguous()
+    q = torch.randn(4, 4, D, generator=g, device=dev).to(BF16)
+    q[:, ::2] = q[:, 1::2] * -1  # both signs in every element
+    lens = torch.tensor([3, 20, 30, 40], dtype=torch.int32, device=dev)
+    out, lse = w4.attn_decode(q, kc, vc, table, lens, k_scales=ks, v_scales=vs, return_lse=True)
+    bad = torch.tensor([[0, 0], [1, 0], [1, 1], [1, 1]], dtype=torch.bool, device=dev).repeat_interleave(2, 1)
+    assert torch.equal(torch.isnan(lse), bad)
+    assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(out).any(-1), bad)
