@@ -256,22 +256,23 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a, con
             float bad = group_max<LANES>(nan ? 1.0f : 0.0f);
             const float amax_c = clamp_amax(amax);
             const float inv = recip448(amax_c);
-            uint32_t q[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                q[i] = cvt_e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
-            // infinity times 0 and NaN, which the conversion's clamp takes for -448: their code is NaN's
-            if (__any(amax == __builtin_inff())) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (!(fabsf(f[2 * i]) < __builtin_inff()))
-                        q[i] = (q[i] & 0xFF00u) | 0x7Fu;
-                    if (!(fabsf(f[2 * i + 1]) < __builtin_inff()))
-                        q[i] = (q[i] & 0xFFu) | 0x7F00u;
-                }
-            }
+            const bool far = __any(amax == __builtin_inff());
             if (!is_q && live) {
                 uint8_t* dst = (uint8_t*)out.p + at;
+                uint32_t q[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    q[i] = cvt_e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
+                // infinity times 0 and NaN, which the conversion's clamp takes for -448: their code is NaN's
+                if (__builtin_expect(far, 0)) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (!(fabsf(f[2 * i]) < __builtin_inff()))
+                            q[i] = (q[i] & 0xFF00u) | 0x7Fu;
+                        if (!(fabsf(f[2 * i + 1]) < __builtin_inff()))
+                            q[i] = (q[i] & 0xFFu) | 0x7F00u;
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     if (e[j] < a.D)
