@@ -3,7 +3,7 @@
 //
 // Bound by the cache's bytes, each read once for up to 16 query heads of its kv
 // head (each 16 more read them again: 64 x 4096 keys, one kv head of 128, bf16,
-// 16 query heads 32 us, 32 52, 128 152).  A wave takes tiles of 32 keys and keeps
+// 16 query heads 32 us, 32 52, 128 154).  A wave takes tiles of 32 keys and keeps
 // everything in registers:
 //   S[key, head] = K Q^T and O[d, head] += V^T P^T are MFMA 16x16x32 with the
 //   heads (up to 16) as columns, so a lane holds one head's scores and sums
@@ -27,10 +27,10 @@
 // one is finished there.  Where sequences are short by the table or the window (`cuts`),
 // a workgroup takes one sequence and kv head whole, and there is no second launch.
 //
-// 64 x 4096 keys, 64 / 8 heads of 128, bf16: 195 us (5.5 TB/s; a reduction reads
-// 6.1) and 4.7 for the second launch, which finds nothing to join; 655 MB of e4m3
-// in 16 sequences: 137 + 6.8 (rows of 128 bytes, 1 KB apart); one sequence of
-// 1000: 7.8 + 4.7.
+// 64 x 4096 keys, 64 / 8 heads of 128, bf16: 192 us (5.6 TB/s; a reduction reads
+// 6.1) and 4.9 for the second launch, which finds nothing to join; 655 MB of e4m3
+// in 16 sequences: 133 + 7.0 (rows of 128 bytes, 1 KB apart); one sequence of
+// 1000: 7.2 + 4.8.
 #include "api_util.hpp"
 #include "common.hpp"
 #include "internal.hpp"
